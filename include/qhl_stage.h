@@ -346,11 +346,167 @@ int qhl_deltanet_step(int Hk, int Hv, const float* y_dev, int n_tok, const float
 int qhl_qgemv_noalloc(int qtype, int rows, int cols, const void* packed_dev, const float* x_dev, int n_tok,
                       float* y_dev, void* stream);
 
-/* Wait for `stream`, then report and clear the device-side error word of the
- * qhl_qgemv / qhl_qgemv_noalloc kernels on the current device: STAGE_E_DEVICE
- * if one of their bounded waits ran out since the last qhl_sync (their output
- * is then garbage; the tile counters are cleared with the word so that later
- * calls are correct), 0 otherwise.  Allocates nothing. */
+/* ---------------------------------------------------------------------------
+ * Verification of trees of drafted tokens over a paged KV cache.
+ *
+ * Drafts are checked together in one batched pass (SwarmLLM README, feature
+ * list); these calls do that for a tree of alternatives instead of one chain,
+ * for a batch of sequences whose caches share a pool of pages.  The pages of
+ * text name no tree and no paged cache; the arithmetic is that of the stage
+ * (QK-norm, partial RoPE, GQA attention, the gated delta rule).
+ *
+ * A batch of trees: the tokens of entry b are rows q_start[b] ..
+ * q_start[b + 1] - 1 of every per-token tensor (q_start_dev: int32
+ * [n_batch + 1], ascending, at most max_nodes rows each).  Rows that belong to
+ * no entry are neither read nor written.  parent_dev: int32 [n_rows], for each
+ * token the index of its parent within its own tree, smaller than its own
+ * index; -1: its parent is the last cached token; -2: a padded token.  A token
+ * sees the cached rows, its ancestors and itself.  A padded token and its
+ * descendants see nothing: their outputs are 0.  One token per sequence with
+ * parent -1 is plain decoding.
+ *
+ * Indices that live on the device are checked there: one that is out of range
+ * is not followed (what it stands for is treated as absent) and qhl_sync
+ * reports it as STAGE_E_DEVICE.  Every call is asynchronous on `stream`, works
+ * on the current device, allocates nothing on the device and may be captured
+ * into a graph (make one call before the first capture: it looks up the error
+ * word and sets kernel attributes).
+ * ------------------------------------------------------------------------- */
+
+/* 16- and 32-bit element types. */
+typedef enum { QHL_F32 = 0, QHL_F16 = 1, QHL_BF16 = 2 } qhl_dtype;
+
+/* A KV cache in pages.  Element (layer, page, head, row, d) of k_dev and of
+ * v_dev is at layer * stride_layer + page * stride_page + head * stride_head +
+ * row * stride_row + d (in elements): any order of the axes, a stage's
+ * contiguous [kv_heads, max_ctx, dim] cache included (stride_page = page_rows *
+ * dim).  Strides are multiples of 8 elements, the bases 16-byte aligned, and
+ * rows of one page do not overlap.  dtype QHL_F16 or QHL_BF16; dim 64, 128 or
+ * 256; page_rows 16, 32, 64, 128 or 256.
+ * Sequence s (0 <= s < n_seqs) has len_dev[s] committed rows, row r in page
+ * table_dev[s * max_pages + r / page_rows], and holds the first held_dev[s]
+ * pages of its table row (len <= held * page_rows).  refs_dev[p] counts the
+ * sequences that hold page p; 0 is a free page. */
+typedef struct {
+  void* k_dev;
+  void* v_dev;
+  int dtype;
+  int n_layers, n_pages, kv_heads, page_rows, dim;
+  long long stride_layer, stride_page, stride_head, stride_row;
+  int n_seqs, max_pages;
+  int* table_dev;
+  int* len_dev;
+  int* held_dev;
+  int* refs_dev;
+} qhl_kv_pages;
+
+/* Norm of every query and key head and rotation by position in one pass, from
+ * the rows an in-projection leaves: y_dev [n_rows] rows of y_stride elements of
+ * y_dtype (QHL_F32, QHL_F16 or QHL_BF16) with the query heads at q_off, the
+ * key heads at k_off and the value heads at v_off (heads of `dim` elements,
+ * 64, 128 or 256, one after the other).  q and k: x / sqrt(mean(x^2) + eps) *
+ * gamma (gamma_q_dev, gamma_k_dev f32 [dim]), then rotate-half RoPE on the
+ * leading rope_dims (a multiple of 8, at most dim; 0: none): the pair
+ * (i, i + rope_dims / 2) turns by pos * theta^(-2 i / rope_dims), with the
+ * angle formed in 64 bits so that far positions keep their phase.  v is
+ * rounded only.  All arithmetic is f32, rounded once to `dtype` (QHL_F16 or
+ * QHL_BF16).  Outputs: q_dev rows of q_stride elements holding [n_q_heads][dim],
+ * k_dev and v_dev [n_kv_heads][dim] with k_stride and v_stride.  pos_dev: int32
+ * [n_rows].  Every base, row and offset is a multiple of 16 bytes. */
+int qhl_qk_norm_rope(int n_q_heads, int n_kv_heads, int dim, int rope_dims, double theta, float eps,
+                     const void* y_dev, int y_dtype, long long y_stride, int q_off, int k_off, int v_off,
+                     int n_rows, const int* pos_dev, const float* gamma_q_dev, const float* gamma_k_dev, int dtype,
+                     void* q_dev, long long q_stride, void* k_dev, long long k_stride, void* v_dev,
+                     long long v_stride, void* stream);
+
+/* Bytes of workspace qhl_tree_attention needs for these arguments (0 for
+ * arguments that it refuses).  The workspace is the caller's: 16-byte aligned,
+ * not shared by calls that may overlap, contents irrelevant before and after. */
+size_t qhl_tree_attention_workspace(const qhl_kv_pages* kv, int n_q_heads, int n_rows, int n_batch, int max_nodes);
+
+/* Attention of n_batch trees of drafted tokens over layer `layer` of a paged
+ * cache: tree b reads the len_dev committed rows of sequence seq_dev[b] (int32
+ * [n_batch]; an entry may repeat) and its own tokens' keys and values
+ * k_new_dev, v_new_dev (rows of new_stride elements holding [kv_heads][dim], in
+ * the cache's type; not in the cache yet, so a rejected draft leaves no trace
+ * and shared pages are only read).  q_dev: rows of q_stride elements holding
+ * [n_q_heads][dim] in the cache's type; query head j reads KV head
+ * j / (n_q_heads / kv_heads).  out = softmax(scale * q k^T) v over the rows the
+ * token sees; out_dev rows of out_stride elements.  lse_dev (or NULL): f32
+ * [n_rows][n_q_heads], the natural logarithm of the sum of exp(scale * q k^T),
+ * -inf where nothing is seen.  A hidden draft's infinities and NaN do not reach
+ * the tokens that do not see it, nor do those of cache rows beyond len.
+ * n_batch 1..2048, max_nodes 1..128, n_q_heads / kv_heads at most 128, scale
+ * positive.  Every base is 16-byte aligned and every stride a multiple of 8.
+ * Scores, softmax statistics and sums are f32; the softmax weights are rounded
+ * to the cache's type for the product with v. */
+int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_rows, int n_batch, int max_nodes,
+                       const int* seq_dev, const int* q_start_dev, const int* parent_dev, const void* q_dev,
+                       long long q_stride, const void* k_new_dev, const void* v_new_dev, long long new_stride,
+                       void* out_dev, long long out_stride, float* lse_dev, float scale, void* workspace_dev,
+                       size_t workspace_bytes, void* stream);
+
+/* The gated DeltaNet step of qhl_deltanet_step along trees: token t of tree b
+ * starts from the state of its parent (for parent -1, state state_index_dev[b]
+ * of states_dev f32 [n_states, Hv, 128, 128]; -1 there: the zero state) and
+ * leaves its own in snaps_dev f32 [n_rows, Hv, 128, 128], so that the state
+ * after any accepted path is the snapshot of its last token.  y_dev and o_dev
+ * as in qhl_deltanet_step, with n_rows rows.  A padded token's o row is 0 and
+ * its snapshot is not written.  Along a path the results are bit-identical to
+ * qhl_deltanet_step.  The snapshots must not overlap the states that are read.
+ * n_batch 1..2048, max_nodes 1..128; y_dev, states_dev, snaps_dev and o_dev
+ * 16-byte aligned, 2 * Hv + the q, k, v widths a multiple of 4. */
+int qhl_deltanet_tree(int Hk, int Hv, const float* y_dev, int n_rows, int n_batch, int max_nodes,
+                      const int* q_start_dev, const int* parent_dev, const float* states_dev, int n_states,
+                      const int* state_index_dev, float* snaps_dev, float* o_dev, void* stream);
+
+/* The pages of a cache.  Each call serves n sequences (1..1024) named by device
+ * arrays int32 [n] and writes a stage_status for each into status_dev int32
+ * [n]; a request that fails changes nothing.  Results do not depend on timing:
+ * requests count in their order, and new pages are the free ones of the lowest
+ * numbers.  A sequence named again in the same call fails with STAGE_E_ARG, as
+ * does a number out of range.
+ *
+ * qhl_pages_free: the sequence lets go of its pages (held and len become 0, its
+ * table row -1); pages that nobody else holds are free.
+ *
+ * qhl_pages_fork: dst[i], which must hold nothing (STAGE_E_STATE), becomes a
+ * copy of src[i] that shares the pages of its committed rows.  Several dst may
+ * have one src; a src that is also a dst of the call fails with STAGE_E_ARG.
+ *
+ * qhl_pages_extend: makes room for add[i] >= 0 more rows: afterwards rows len ..
+ * len + add - 1 are in pages that the sequence alone holds.  A shared page that
+ * holds the next row is replaced by a new one and its committed rows are copied
+ * in every layer, unless the other holders, earlier in the call, have let go of
+ * it; then new pages follow.  Fails with STAGE_E_OOM where the pool has too few
+ * free pages (so do the later requests of the call that need a page or share
+ * their last one), STAGE_E_ARG where the table row is too short, STAGE_E_STATE
+ * where a later page in the range is shared.  workspace_dev: 16 * n bytes.
+ *
+ * qhl_pages_commit: the accepted path of each tree into the cache: rows pos[b]
+ * .. pos[b] + n_accepted[b] - 1 of sequence seq[b] become rows q_start[b] +
+ * path[b * path_stride + j] of k_new_dev, v_new_dev (element (layer, row, head,
+ * d) at layer * new_stride_layer + row * new_stride_row + head * dim + d) in
+ * every layer, and its length pos + n_accepted.  pos is at most the length
+ * (smaller takes the sequence back to pos).  Fails with STAGE_E_ARG for a path
+ * entry outside its tree, n_accepted outside 0..path_stride or above 128, or
+ * pos out of range; STAGE_E_STATE where the sequence does not hold the pages
+ * alone (extend first). */
+int qhl_pages_free(const qhl_kv_pages* kv, int n, const int* seq_dev, int* status_dev, void* stream);
+int qhl_pages_fork(const qhl_kv_pages* kv, int n, const int* src_dev, const int* dst_dev, int* status_dev,
+                   void* stream);
+int qhl_pages_extend(const qhl_kv_pages* kv, int n, const int* seq_dev, const int* add_dev, int* status_dev,
+                     void* workspace_dev, size_t workspace_bytes, void* stream);
+int qhl_pages_commit(const qhl_kv_pages* kv, int n_batch, int n_rows, const int* seq_dev, const int* q_start_dev,
+                     const int* path_dev, int path_stride, const int* n_accepted_dev, const int* pos_dev,
+                     const void* k_new_dev, const void* v_new_dev, long long new_stride_layer,
+                     long long new_stride_row, int* status_dev, void* stream);
+
+/* Wait for `stream`, then report and clear the device-side error words of the
+ * qhl_* kernels on the current device: STAGE_E_DEVICE if a bounded wait ran out
+ * since the last qhl_sync (the output is then garbage; the GEMV's tile counters
+ * are cleared with the word so that later calls are correct) or an index that
+ * lives on the device was out of range, 0 otherwise.  Allocates nothing. */
 int qhl_sync(void* stream);
 
 /* Failure injection for tests of that error path (no counterpart on the

@@ -16,6 +16,7 @@ namespace qhl {
 thread_local std::string g_last_error;
 void set_last_error(const std::string& s) { g_last_error = s; }
 unsigned noalloc_take_error(int dev);   // noalloc.cu: read and clear the static scratch's error word
+unsigned verify_take_error(int dev);    // pages.cu: read and clear the verify operators' error word
 }  // namespace qhl
 
 namespace {
@@ -228,7 +229,10 @@ int qhl_sync(void* stream) {
     }
   }
   word |= noalloc_take_error(dev);
-  if (word) return err(STAGE_E_DEVICE, "device error word " + std::to_string(word) + " (bounded wait timed out)");
+  word |= verify_take_error(dev);
+  if (word)
+    return err(STAGE_E_DEVICE, "device error word " + std::to_string(word) +
+                                   (word & 4u ? " (an index on the device was out of range)" : " (bounded wait timed out)"));
   return 0;
 }
 

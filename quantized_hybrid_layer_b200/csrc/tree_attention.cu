@@ -1,0 +1,1063 @@
+// qhl_tree_attention: attention of trees of drafted tokens over a paged cache.
+//
+// For a query row q (token i, head j, KV head j / G) over the keys it sees:
+//     s = scale * q . k,   out = sum exp(s - m) v / sum exp(s - m),   m a running maximum,
+// in one pass over the keys, a tile of KT keys at a time:
+//     S = Q K^T (f32 in tensor memory), p = 2^(c S - c m) with c = scale / ln 2,
+//     O += p V (f32 in tensor memory), l += sum p.
+// m is raised only when a tile's maximum exceeds it by more than 2^8 in p (the
+// result does not depend on m; p stays below 2^8, far inside f16's range), so O
+// is seldom rescaled.  p is rounded to the cache's type for the product; l adds
+// the unrounded p.
+//
+// What bounds it: for few query rows the bytes of K and V (one byte of cache
+// feeds 2 query rows x 2 operations per element; a tile of 128 rows needs about
+// half the tensor core's rate at HBM's), for many the products.  Both products
+// run on tcgen05 with M = 128 query rows: all tokens x query heads of one KV
+// head, so a cache row is read once for all of them (a tree with more rows takes
+// several M tiles, whose CTAs read the same tiles at the same time, from L2).
+// A tile of 64 keys x 256 dimensions (128 x 128, 128 x 64) is one 32 KB slot of
+// a ring filled by TMA; p stays in tensor memory, over the S it came from, as
+// the A operand of the second product.
+//
+// Work split: an item is (tree, KV head, M tile, range of key tiles).  A small
+// planning kernel picks the tiles per item so that the items fill the SMs in
+// few even waves; items of a split range leave (O, m, l) in the workspace and a
+// third kernel joins them in the order of the ranges.  Lengths are read on the
+// device, so one captured graph serves every length.
+//
+// Roles of a CTA (one per SM): warps 0-7 softmax (warp w: the 32 rows of lane
+// quarter w % 4 and half w / 4 of the keys; O's columns are halved the same way),
+// warp 8 TMA, warp 9 one MMA issuer, warps 10-11 ancestor masks and the tiles
+// that need care.  Rows of V that nobody may see (beyond the sequence, beyond
+// the tree, in pages of garbage) are zeroed in shared memory, since 0 * NaN is
+// NaN; a drafted V row's infinities and NaN are taken out the same way and put
+// back, at the end, into the rows of the tokens that see them.
+#include <algorithm>
+#include <mutex>
+
+#include "launch.h"
+#include "tc5_f16.cuh"
+#include "verify.cuh"
+
+namespace qhl {
+
+// ------------------------------------------------------------------- shapes --
+
+constexpr int kTaThreads = 384;
+constexpr uint32_t kTaWait = 1u << 22;   // tries of a wait before it is given up (seconds)
+constexpr int kTaRows = 128;          // rows of an M tile
+constexpr int kTaWaves = 8;           // planned waves beyond the fewest possible
+constexpr int kTaSplitItems = 4;      // at most this many split items per SM
+
+template <int DIM>
+struct TaShape {
+  static constexpr int KT = DIM == 256 ? 64 : 128;     // keys per tile
+  static constexpr int CH = DIM / 64;                  // 128-byte chunks of a row
+  static constexpr int SLOT = KT * DIM * 2;            // bytes of a ring slot
+  static constexpr int NS = DIM == 256 ? 4 : DIM == 128 ? 5 : 8;
+  static constexpr int QB = kTaRows * DIM * 2;
+  static constexpr int SMEM = 1024 + QB + NS * SLOT;   // 1024: room to align the swizzle atoms
+};
+
+// One tree as the plan sees it.
+struct TaSeq {
+  int row0, n, seq, ctx;
+  int chunks;        // ranges its key tiles are split into
+  int slot0;         // its first partial row
+  int wide;          // which of the two M tilings
+  int tiles;
+};
+
+// An M tiling: gb query heads x nb tokens of one KV head.
+struct TaTiling {
+  int gb, nb, ng;    // ng = ceil(G / gb)
+};
+
+struct TaArgs {
+  CUtensorMap q[2];            // per tiling
+  CUtensorMap k, v;            // cache pages
+  CUtensorMap kn, vn;          // drafted rows
+  TaTiling tiling[2];
+  int box, dbox;               // rows per TMA box of a page / of drafted rows
+  int page_rows, n_pages, max_pages, n_seqs;
+  int Hkv, G, n_rows, n_batch, max_nodes;
+  const int* table;
+  const int* len;
+  const int* seq;
+  const int* q_start;
+  const int* parent;
+  const void* v_new;
+  long long new_stride;
+  void* out;
+  long long out_stride;
+  float* lse;
+  float c;                     // scale / ln 2
+  int* hdr;                    // [0]: items
+  TaSeq* seqs;
+  int4* items;                 // tree, first tile, last tile + 1, head | m tile << 8 | range << 16
+  float2* pml;                 // per partial row: c m, l
+  float* po;                   // per partial row: O
+  int grid;
+  unsigned* err;
+};
+
+// ------------------------------------------------------------------ planning --
+
+template <int DIM>
+__global__ void __launch_bounds__(512) tree_plan_kernel(const __grid_constant__ TaArgs a) {
+  constexpr int KT = TaShape<DIM>::KT;
+  __shared__ int s_nt[kMaxBatch], s_nm[kMaxBatch], s_end[kMaxBatch];
+  __shared__ int s_w[2][16];
+  __shared__ int s_lc[kTaWaves];
+  __shared__ long long s_cost[kTaWaves];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) pdl_launch();
+  int longest = 0, whole = 0;
+  for (int b = tid; b < a.n_batch; b += 512) {
+    TaSeq s;
+    tree_rows(a.q_start, b, a.n_rows, a.max_nodes, s.row0, s.n, a.err);
+    s.seq = __ldg(a.seq + b);
+    s.ctx = 0;
+    if (s.seq < 0 || s.seq >= a.n_seqs) {
+      atomicOr(a.err, ERR_BAD_INDEX);
+      s.seq = 0;
+    } else {
+      s.ctx = a.len[s.seq];
+      if (s.ctx < 0 || s.ctx > (long long)a.max_pages * a.page_rows) {
+        atomicOr(a.err, ERR_BAD_INDEX);
+        s.ctx = 0;
+      }
+    }
+    s.wide = s.n > a.tiling[0].nb;
+    s.tiles = s.n ? (s.ctx + KT - 1) / KT + (s.n + KT - 1) / KT : 0;
+    s.chunks = s.slot0 = 0;
+    const TaTiling t = a.tiling[s.wide];
+    const int nm = s.n ? t.ng * ((s.n + t.nb - 1) / t.nb) : 0;
+    a.seqs[b] = s;
+    s_nt[b] = s.tiles;
+    s_nm[b] = nm * a.Hkv;
+    longest = max(longest, s.tiles);
+    whole += nm * a.Hkv;
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  whole = __reduce_add_sync(0xffffffffu, whole);
+  if (lane == 0) {
+    s_w[0][warp] = longest;
+    s_w[1][warp] = whole;
+  }
+  __syncthreads();
+  longest = whole = 0;
+  for (int i = 0; i < 16; ++i) {
+    longest = max(longest, s_w[0][i]);
+    whole += s_w[1][i];
+  }
+  // Warp w: the fewest tiles per item such that the items fit w0 + w waves of
+  // the grid (w0: the fewest waves possible) and the split ones the workspace;
+  // its cost in tiles, with about two tiles' time for an item's start and end.
+  const int w0 = (whole + a.grid - 1) / a.grid;
+  if (warp < kTaWaves) {
+    int lo = 1, hi = max(longest, 1);
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      int items = 0, split = 0;
+      for (int b = lane; b < a.n_batch; b += 32) {
+        const int x = (s_nt[b] + mid - 1) / mid * s_nm[b];
+        items += min(x, 1 << 20);
+        split += s_nt[b] > mid ? min(x, 1 << 20) : 0;
+      }
+      items = __reduce_add_sync(0xffffffffu, items);
+      split = __reduce_add_sync(0xffffffffu, split);
+      if (items >= 0 && split >= 0 && items <= (w0 + warp) * a.grid && split <= kTaSplitItems * a.grid)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    if (lane == 0) {
+      s_lc[warp] = lo;
+      s_cost[warp] = (long long)max(w0 + warp, 1) * (lo + 2);
+    }
+  }
+  __syncthreads();
+  int best = 0;
+  for (int i = 1; i < kTaWaves; ++i)
+    if (s_cost[i] < s_cost[best]) best = i;
+  const int lc = s_lc[best];
+  // prefix sums of the items and of the partial rows, 512 trees at a time
+  int items = 0, slots = 0;
+  for (int base = 0; base < a.n_batch; base += 512) {
+    const int b = base + tid;
+    int x = 0, y = 0, chunks = 0;
+    if (b < a.n_batch) {
+      chunks = (s_nt[b] + lc - 1) / lc;
+      x = chunks * s_nm[b];
+      y = chunks > 1 ? chunks * a.Hkv * a.seqs[b].n * a.G : 0;
+    }
+    int ix = x, iy = y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, ix, o), v = __shfl_up_sync(0xffffffffu, iy, o);
+      if (lane >= o) {
+        ix += u;
+        iy += v;
+      }
+    }
+    __syncthreads();
+    if (lane == 31) {
+      s_w[0][warp] = ix;
+      s_w[1][warp] = iy;
+    }
+    __syncthreads();
+    int tx = 0, ty = 0;
+    for (int i = 0; i < 16; ++i) {
+      if (i == warp) {
+        ix += tx;
+        iy += ty;
+      }
+      tx += s_w[0][i];
+      ty += s_w[1][i];
+    }
+    if (b < a.n_batch) {
+      s_end[b] = items + ix;
+      a.seqs[b].chunks = chunks;
+      a.seqs[b].slot0 = slots + iy - y;
+    }
+    items += tx;
+    slots += ty;
+  }
+  __syncthreads();
+  if (tid == 0) a.hdr[0] = items;
+  for (int i = tid; i < items; i += 512) {
+    int lo = 0, hi = a.n_batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (s_end[mid] > i) hi = mid;
+      else lo = mid + 1;
+    }
+    const int nt = s_nt[lo], chunks = (nt + lc - 1) / lc, nm = s_nm[lo] / a.Hkv;
+    int r = i - (s_end[lo] - chunks * s_nm[lo]);
+    const int mt = r % nm;
+    r /= nm;
+    const int h = r % a.Hkv, ck = r / a.Hkv;
+    a.items[i] = make_int4(lo, (int)((long long)ck * nt / chunks), (int)((long long)(ck + 1) * nt / chunks), h | mt << 8 | ck << 16);
+  }
+}
+
+// ---------------------------------------------------------------- attention --
+
+template <bool BF16>
+QHL_DEV uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool BF16>
+QHL_DEV bool non_finite16(uint32_t h) {
+  return BF16 ? (h & 0x7f80u) == 0x7f80u : (h & 0x7c00u) == 0x7c00u;
+}
+template <bool BF16>
+QHL_DEV float widen16(uint32_t h) {
+  return BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+}
+
+// A wait names a phase by its parity, so a waiter must not be two phases away
+// from it.  The softmax warps wait for the product with V only when they rescale
+// and at an item's end; pv_done is kept per tile parity for them: when S of tile
+// T is there, the product of tile T - 2, issued before it, is complete.
+struct TaBars {
+  uint64_t full[8], empty[8], vok[8];
+  uint64_t q_full, q_empty, s_full[2], p_ready[2], pv_done[2], mask_full, mask_empty;
+};
+
+// What the roles know of an item.
+struct TaItem {
+  TaSeq s;
+  int t0, t1, h, ck, n0, g0, nct;   // n0, g0: the M tile's first token and query head; nct: cache tiles
+};
+
+template <int DIM>
+QHL_DEV TaItem ta_item(const TaArgs& a, int i) {
+  const int4 it = __ldcg(a.items + i);
+  TaItem r;
+  const int4* s = reinterpret_cast<const int4*>(a.seqs + it.x);
+  const int4 s0 = __ldcg(s), s1 = __ldcg(s + 1);
+  r.s = TaSeq{s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+  r.t0 = it.y;
+  r.t1 = it.z;
+  r.h = it.w & 255;
+  r.ck = it.w >> 16;
+  const int mt = it.w >> 8 & 255;
+  const TaTiling& t = a.tiling[r.s.wide];
+  r.g0 = mt % t.ng * t.gb;
+  r.n0 = mt / t.ng * t.nb;
+  r.nct = (r.s.ctx + TaShape<DIM>::KT - 1) / TaShape<DIM>::KT;
+  return r;
+}
+
+template <int DIM, bool BF16>
+__global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_constant__ TaArgs a) {
+  using Sh = TaShape<DIM>;
+  constexpr int KT = Sh::KT, CH = Sh::CH, NS = Sh::NS, HK = KT / 2;
+  constexpr uint32_t kS0 = 256;                      // tensor-memory columns: O at 0, S at 256 and 256 + KT
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TaBars bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ __align__(16) uint4 s_anc[kMaxNodes];   // per token: the tokens it sees, a bit each
+  __shared__ int s_jump[kMaxNodes];
+  __shared__ unsigned s_bad[4];                      // tokens whose V row holds an infinity or NaN
+  __shared__ float s_max[2][2][kTaRows], s_sum[2][kTaRows];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sq = (smem_u32(smem_raw) + 1023u) & ~1023u, ring = sq + Sh::QB;
+  auto bar = [](const uint64_t& b) { return smem_u32(&b); };
+
+  if (tid == 0) {
+    pdl_launch();
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bar(bars.full[i]), 1);
+      mbar_init(bar(bars.empty[i]), 1);
+      mbar_init(bar(bars.vok[i]), 2);
+    }
+    mbar_init(bar(bars.q_full), 1);
+    mbar_init(bar(bars.q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(bars.s_full[i]), 1);
+      mbar_init(bar(bars.p_ready[i]), 8);
+      mbar_init(bar(bars.pv_done[i]), 1);
+    }
+    mbar_init(bar(bars.mask_full), 2);
+    mbar_init(bar(bars.mask_empty), 8);
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(&s_tmem, 512);
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_map(&a.k);
+    tma_prefetch_map(&a.v);
+    tma_prefetch_map(&a.kn);
+    tma_prefetch_map(&a.vn);
+    tma_prefetch_map(&a.q[0]);
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+  const int n_items = __ldcg(a.hdr);
+  // Every wait is bounded; a role that gave one up stops (ok = false) once those
+  // it shares a named barrier with know it too.
+  bool ok = true;
+  auto wait_warp = [&](const uint64_t& b, uint32_t parity) {   // the same answer in every lane
+    return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, a.err, kTaWait)) != 0;
+  };
+
+  if (warp == 8) {
+    // ---------------------------------------------------------------- TMA --
+    uint32_t r = 0, it = 0;
+    auto acquire = [&](uint32_t bytes) {             // the next slot, once its last contents are used
+      const uint32_t s = r % NS, ph = r / NS & 1;
+      ok = wait_warp(bars.empty[s], ph ^ 1);
+      if (lane == 0 && ok) mbar_arrive_expect_tx(bar(bars.full[s]), bytes);
+      ++r;
+      return s;
+    };
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x, ++it) {
+      const TaItem w = ta_item<DIM>(a, i);
+      const TaTiling& t = a.tiling[w.s.wide];
+      const int* row = a.table + (size_t)w.s.seq * a.max_pages;
+      // page numbers of this item's boxes, 32 at a time, one batch ahead
+      const int boxes_per_tile = KT / a.box, box_end = (w.s.ctx + a.box - 1) / a.box;
+      int jb = w.t0 * boxes_per_tile;
+      auto page_of = [&](int j) {
+        int pg = -1;
+        if (j < box_end) {
+          pg = __ldg(row + (int)((long long)j * a.box / a.page_rows));
+          if (pg < 0 || pg >= a.n_pages) {
+            atomicOr(a.err, ERR_BAD_INDEX);
+            pg = a.n_pages;                          // beyond the tensor: the copy fills zeros
+          }
+        }
+        return pg;
+      };
+      int ids = page_of(jb + lane), ids_next = page_of(jb + 32 + lane), ids_at = jb;
+
+      if (!(ok = wait_warp(bars.q_empty, (it & 1) ^ 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(bars.q_full), CH * t.gb * t.nb * 128);
+        for (int c = 0; c < CH; ++c)
+          tma_load_5d(sq + c * kTaRows * 128, &a.q[w.s.wide], bar(bars.q_full), w.g0, w.s.row0 + w.n0, c, w.h);
+      }
+      for (int tile = w.t0; ok && tile < w.t1; ++tile) {
+        if (tile < w.nct) {
+          const int nb = min(boxes_per_tile, box_end - tile * boxes_per_tile);
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            const uint32_t s = acquire((uint32_t)nb * a.box * DIM * 2);
+            if (!ok) break;
+            const uint32_t dst = ring + s * Sh::SLOT;
+            const CUtensorMap* map = kv ? &a.v : &a.k;
+            for (int j = 0; j < nb; ++j) {
+              const int jj = tile * boxes_per_tile + j;
+              if (jj - ids_at >= 32) {               // tiles never straddle a batch: 32 is a multiple of their boxes
+                ids = ids_next;
+                ids_at += 32;
+                ids_next = page_of(ids_at + 32 + lane);
+              }
+              const int pg = __shfl_sync(0xffffffffu, ids, jj - ids_at);
+              if (lane == 0) {
+                const int rr = (int)((long long)jj * a.box % a.page_rows);
+                if (a.box == KT) {
+                  tma_load_5d(dst, map, bar(bars.full[s]), rr, 0, w.h, pg);
+                } else {
+                  for (int c = 0; c < CH; ++c)
+                    tma_load_5d(dst + c * KT * 128 + j * a.box * 128, map, bar(bars.full[s]), rr, c, w.h, pg);
+                }
+              }
+            }
+          }
+        } else {
+          const int rr = w.s.row0 + (tile - w.nct) * KT;
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            const uint32_t s = acquire((uint32_t)a.dbox * DIM * 2);
+            if (!ok || lane) continue;
+            const uint32_t dst = ring + s * Sh::SLOT;
+            const CUtensorMap* map = kv ? &a.vn : &a.kn;
+            if (a.dbox == KT) {
+              tma_load_5d(dst, map, bar(bars.full[s]), rr, 0, w.h, 0);
+            } else {
+              for (int c = 0; c < CH; ++c) tma_load_5d(dst + c * KT * 128, map, bar(bars.full[s]), rr, c, w.h, 0);
+            }
+          }
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- MMA --
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_f16(BF16, false, kTaRows, KT), id_pv = idesc_f16(BF16, true, kTaRows, DIM);
+      uint32_t r = 0, T = 0, it = 0, vok_phase = 0;
+      bool have = false, p_first = false, p_care = false;
+      uint32_t p_T = 0, p_r = 0;
+      auto pv = [&]() {                              // the product with V of the tile before
+        const uint32_t b = p_T & 1, s = p_r % NS;
+        if (!mbar_wait(bar(bars.p_ready[b]), p_T >> 1 & 1, a.err, kTaWait)) return false;
+        if (!mbar_wait(bar(bars.full[s]), p_r / NS & 1, a.err, kTaWait)) return false;
+        if (p_care) {
+          if (!mbar_wait(bar(bars.vok[s]), vok_phase >> s & 1, a.err, kTaWait)) return false;
+          vok_phase ^= 1u << s;
+        }
+        tc_fence_after();
+        const uint32_t p = tmem + kS0 + b * KT;
+        const uint64_t vd = smem_desc_sw128(ring + s * Sh::SLOT, KT * 128);
+#pragma unroll
+        for (int k = 0; k < KT / 16; ++k) mma_f16_ts(tmem, p + k * 8, vd + (uint64_t)(k * 2048 >> 4), id_pv, !p_first || k);
+        tc_commit(&bars.empty[s]);
+        tc_commit(&bars.pv_done[b]);
+        return true;
+      };
+      for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x, ++it) {
+        const TaItem w = ta_item<DIM>(a, i);
+        if (!(ok = mbar_wait(bar(bars.q_full), it & 1, a.err, kTaWait))) break;
+        for (int tile = w.t0; tile < w.t1; ++tile, ++T, r += 2) {
+          const uint32_t s = r % NS, b = T & 1;
+          if (!(ok = mbar_wait(bar(bars.full[s]), r / NS & 1, a.err, kTaWait))) break;
+          tc_fence_after();
+          const uint64_t qd = smem_desc_sw128(sq, 16), kd = smem_desc_sw128(ring + s * Sh::SLOT, 16);
+#pragma unroll
+          for (int k = 0; k < DIM / 16; ++k)
+            mma_f16_ss(tmem + kS0 + b * KT, qd + (uint64_t)((k / 4) * (kTaRows * 128) + (k % 4) * 32 >> 4),
+                       kd + (uint64_t)((k / 4) * (KT * 128) + (k % 4) * 32 >> 4), id_qk, k != 0);
+          tc_commit(&bars.s_full[b]);
+          tc_commit(&bars.empty[s]);
+          if (tile == w.t1 - 1) tc_commit(&bars.q_empty);
+          if (have && !(ok = pv())) break;
+          have = true;
+          p_T = T;
+          p_r = r + 1;
+          p_first = tile == w.t0;
+          p_care = tile >= w.nct || (tile + 1) * KT > w.s.ctx;
+        }
+      }
+      if (ok && have) pv();
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ------------------------------------------- masks, tiles that need care --
+    const int ft = tid - 320;                        // 0..63
+    uint32_t r = 0, it = 0;
+    for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++it) {
+      const TaItem w = ta_item<DIM>(a, i);
+      const int n = w.s.n;
+      if (ok && it) ok = wait_warp(bars.mask_empty, (it - 1) & 1);
+      if (!(ok = bar_and(6, 64, ok))) break;
+      if (ft < 4) s_bad[ft] = 0;
+      // ancestors by doubling: after k rounds those up to 2^k steps away; a jump
+      // ends at -1 (the cached sequence) or -2 (padded: nothing is seen)
+      for (int x = ft; x < n; x += 64) {
+        int p = __ldg(a.parent + w.s.row0 + x);
+        if (p < -2 || p >= x) {
+          atomicOr(a.err, ERR_BAD_INDEX);
+          p = -2;
+        }
+        s_jump[x] = p;
+        uint32_t m[4] = {0, 0, 0, 0};
+        m[x >> 5] = 1u << (x & 31);
+        s_anc[x] = make_uint4(m[0], m[1], m[2], m[3]);
+      }
+      named_sync(6, 64);
+      for (int step = 1; step < n; step <<= 1) {
+        uint4 m[2];
+        int jp[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int x = ft + 64 * u;
+          jp[u] = -1;
+          if (x < n) {
+            m[u] = s_anc[x];
+            jp[u] = s_jump[x];
+            if (jp[u] >= 0) {
+              const uint4 o = s_anc[jp[u]];
+              m[u] = make_uint4(m[u].x | o.x, m[u].y | o.y, m[u].z | o.z, m[u].w | o.w);
+              jp[u] = s_jump[jp[u]];
+            }
+          }
+        }
+        named_sync(6, 64);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (ft + 64 * u < n) {
+            s_anc[ft + 64 * u] = m[u];
+            s_jump[ft + 64 * u] = jp[u];
+          }
+        named_sync(6, 64);
+      }
+      for (int x = ft; x < n; x += 64)
+        if (s_jump[x] == -2) s_anc[x] = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.mask_full));
+
+      for (int tile = w.t0; ok && tile < w.t1; ++tile, r += 2) {
+        // every tile's V is waited for, so that the wait's parity is that of its phase
+        const bool draft = tile >= w.nct;
+        const uint32_t s = (r + 1) % NS;
+        if (!(ok = wait_warp(bars.full[s], (r + 1) / NS & 1))) break;
+        if (!draft && (tile + 1) * KT <= w.s.ctx) continue;
+        const int dt = tile - w.nct;
+        const int valid = draft ? min(KT, n - dt * KT) : w.s.ctx - tile * KT;
+        uint8_t* base = smem_raw + (ring + s * Sh::SLOT - smem_u32(smem_raw));
+        // units of 16 bytes; the swizzle permutes units within a row only
+        for (int u = ft; u < CH * KT * 8; u += 64) {
+          const int rr = u / 8 % KT;
+          uint4* p = reinterpret_cast<uint4*>(base) + u;
+          if (rr >= valid) {
+            *p = make_uint4(0, 0, 0, 0);
+          } else if (draft) {
+            uint4 x = *p;
+            uint32_t* y = reinterpret_cast<uint32_t*>(&x);
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (non_finite16<BF16>(y[e])) { y[e] &= 0xffff0000u; bad = true; }
+              if (non_finite16<BF16>(y[e] >> 16)) { y[e] &= 0xffffu; bad = true; }
+            }
+            if (bad) {
+              *p = x;
+              const int node = dt * KT + rr;
+              atomicOr(&s_bad[node >> 5], 1u << (node & 31));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars.vok[s]));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- softmax --
+    const int qd = warp & 3, hf = warp >> 2, row = qd * 32 + lane;
+    const uint32_t lanes = (uint32_t)(qd * 32) << 16;
+    const float c = a.c, thr = 8.f / c;
+    uint32_t T = 0, it = 0;
+    for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++it) {
+      const TaItem w = ta_item<DIM>(a, i);
+      const TaTiling& t = a.tiling[w.s.wide];
+      const int nl = row / t.gb, gl = row - nl * t.gb, node = w.n0 + nl, g = w.g0 + gl;
+      const bool valid = nl < t.nb && node < w.s.n && g < a.G;
+      const bool active = __any_sync(0xffffffffu, valid);
+      ok = wait_warp(bars.mask_full, it & 1);
+      uint4 anc = make_uint4(0, 0, 0, 0);
+      if (valid) anc = s_anc[node];
+      const bool alive = (anc.x | anc.y | anc.z | anc.w) != 0;
+      float m = -INFINITY, l = 0.f;
+      bool stop = false;
+
+      for (int tile = w.t0; tile < w.t1; ++tile, ++T) {
+        const uint32_t b = T & 1;
+        if (ok) ok = wait_warp(bars.s_full[b], T >> 1 & 1);
+        if (!active && !ok) {
+          stop = true;
+          break;
+        }
+        if (active) {
+          tc_fence_after();
+          const uint32_t sb = tmem + lanes + kS0 + b * KT;
+          uint32_t sv[HK / 32][32];
+#pragma unroll
+          for (int j = 0; j < HK / 32; ++j) tmem_ld32(sb + hf * HK + 32 * j, sv[j]);
+          tmem_ld_wait();
+          if (tile >= w.nct) {
+            const int w0 = (tile - w.nct) * (KT / 32) + hf * (HK / 32);
+#pragma unroll
+            for (int j = 0; j < HK / 32; ++j) {
+              const int wi = w0 + j;
+              const uint32_t bits = wi == 0 ? anc.x : wi == 1 ? anc.y : wi == 2 ? anc.z : anc.w;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(bits >> e & 1)) sv[j][e] = 0xff800000u;
+            }
+          } else {
+            const int lim = alive ? w.s.ctx - tile * KT - hf * HK : 0;
+            if (lim < HK) {
+#pragma unroll
+              for (int j = 0; j < HK / 32; ++j)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (32 * j + e >= lim) sv[j][e] = 0xff800000u;
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < HK / 32; ++j)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[j][e]));
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          s_max[b][hf][row] = top;
+          ok = bar_and(1 + qd, 64, ok);
+          if (!ok) {
+            stop = true;
+            break;
+          }
+          top = fmaxf(top, s_max[b][hf ^ 1][row]);
+
+          if (tile == w.t0) {
+            m = top;
+          } else {
+            const bool raise = top > m + thr;
+            if (__any_sync(0xffffffffu, raise)) {
+              ok = wait_warp(bars.pv_done[(T - 1) & 1], (T - 1) >> 1 & 1);
+              tc_fence_after();
+              const float al = raise ? ex2((m - top) * c) : 1.f;
+              if (raise) m = top;
+              l *= al;
+#pragma unroll 1
+              for (int j = 0; j < DIM / 64; ++j) {
+                uint32_t o[32];
+                const uint32_t oc = tmem + lanes + hf * (DIM / 2) + 32 * j;
+                tmem_ld32(oc, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                tmem_st32(oc, o);
+              }
+            }
+          }
+          const float ms = m == -INFINITY ? 0.f : m * c;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < HK / 32; ++j) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float p0 = ex2(__fmaf_rn(__uint_as_float(sv[j][e]), c, -ms));
+              const float p1 = ex2(__fmaf_rn(__uint_as_float(sv[j][e + 1]), c, -ms));
+              sum[e & 2] += p0;
+              sum[(e & 2) + 1] += p1;
+              pk[e / 2] = pack2<BF16>(p0, p1);
+            }
+            tmem_st16(sb + hf * (KT / 4) + 16 * j, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars.p_ready[b]));
+      }
+      if (stop) break;
+
+      // ------------------------------------------------------ the item's end --
+      if (ok) ok = wait_warp(bars.pv_done[(T - 1) & 1], (T - 1) >> 1 & 1);
+      if (!active && !ok) break;
+      if (active) {
+        tc_fence_after();
+        s_sum[hf][row] = l;
+        ok = bar_and(1 + qd, 64, ok);
+        if (!ok) break;
+        l += s_sum[hf ^ 1][row];
+        const bool whole = w.s.chunks == 1;
+        const long long slot = w.s.slot0 + ((long long)w.ck * a.Hkv + w.h) * w.s.n * a.G + (long long)node * a.G + g;
+        const float inv = l > 0.f || l != l ? __frcp_rn(l) : 0.f;
+        const bool none = l == 0.f;                  // nothing seen: 0, whatever the tiles held
+        uint32_t bad[4];
+        const uint32_t see[4] = {anc.x, anc.y, anc.z, anc.w};
+        bool any_bad = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          bad[j] = w.t1 > w.nct ? s_bad[j] & see[j] : 0u;
+          any_bad |= bad[j] != 0;
+        }
+        uint8_t* orow = static_cast<uint8_t*>(a.out) + ((long long)(w.s.row0 + node) * a.out_stride + (w.h * a.G + g) * DIM + hf * (DIM / 2)) * 2;
+        float* prow = a.po + slot * DIM + hf * (DIM / 2);
+#pragma unroll 1
+        for (int j = 0; j < DIM / 64; ++j) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(tmem + lanes + hf * (DIM / 2) + 32 * j, o);
+          tmem_ld_wait();
+          if (!valid) continue;
+          if (any_bad) {
+            // drafted V values that are not finite, seen with a positive weight
+            for (int x = 0; x < w.s.n; ++x) {
+              const int word = x >> 5;
+              const uint32_t bw = word == 0 ? bad[0] : word == 1 ? bad[1] : word == 2 ? bad[2] : bad[3];
+              const int dt = x / KT + w.nct;
+              if (!(bw >> (x & 31) & 1) || dt < w.t0 || dt >= w.t1) continue;
+              const uint16_t* vr = static_cast<const uint16_t*>(a.v_new) + (long long)(w.s.row0 + x) * a.new_stride + w.h * DIM + hf * (DIM / 2) + 32 * j;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t h = __ldg(vr + e);
+                if (non_finite16<BF16>(h)) o[e] = __float_as_uint(__uint_as_float(o[e]) + widen16<BF16>(h));
+              }
+            }
+          }
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 x;
+              uint32_t* y = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                y[z] = none ? 0u : pack2<BF16>(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
+              *reinterpret_cast<uint4*>(orow + (32 * j + e) * 2) = x;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(prow + 32 * j + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        if (valid && hf == 0) {
+          const float mc = m == -INFINITY ? -INFINITY : m * c;
+          if (!whole)
+            a.pml[slot] = make_float2(mc, l);
+          else if (a.lse)
+            a.lse[(long long)(w.s.row0 + node) * (a.Hkv * a.G) + w.h * a.G + g] =
+                none ? -INFINITY : (mc + log2f(l)) * 0.69314718055994530942f;
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.mask_empty));
+    }
+  }
+  if (!ok) drain_inflight_copies();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// --------------------------------------------------------------------- join --
+
+// One CTA per (query head, token, tree): the ranges' partials, in their order
+// within each of four groups, and the groups as (0 + 1) + (2 + 3).
+template <int DIM, bool BF16>
+__global__ void __launch_bounds__(DIM) tree_join_kernel(const __grid_constant__ TaArgs a) {
+  constexpr int L = DIM / 4;                         // threads per group, four values each
+  __shared__ float s_wt[kTaSplitItems * 256];
+  __shared__ float s_red[DIM / 32];
+  __shared__ float4 s_o[4][L];
+  const int qh = blockIdx.x, node = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  pdl_wait();
+  const int4* sp = reinterpret_cast<const int4*>(a.seqs + b);
+  const int4 s0 = __ldcg(sp), s1 = __ldcg(sp + 1);
+  const int n = s0.y, chunks = s1.x;
+  if (node >= n || chunks <= 1) return;
+  const int h = qh / a.G, g = qh - h * a.G;
+  const long long step = (long long)a.Hkv * n * a.G;
+  const long long slot = s1.y + (long long)h * n * a.G + (long long)node * a.G + g;
+  float top = -INFINITY;
+  for (int j = tid; j < chunks; j += DIM) {
+    const float2 ml = __ldcg(a.pml + slot + j * step);
+    if (ml.y != 0.f) top = fmaxf(top, ml.x);
+  }
+  top = warp_max(top);
+  if ((tid & 31) == 0) s_red[tid >> 5] = top;
+  __syncthreads();
+  top = s_red[0];
+  for (int j = 1; j < DIM / 32; ++j) top = fmaxf(top, s_red[j]);
+  float sum = 0.f;
+  for (int j = tid; j < chunks; j += DIM) {
+    const float2 ml = __ldcg(a.pml + slot + j * step);
+    const float wt = ml.y != 0.f ? ex2(ml.x - top) : 0.f;   // NaN counts
+    s_wt[j] = ml.y != 0.f ? wt : -1.f;               // -1: a range that saw nothing, not read
+    sum += wt * ml.y;
+  }
+  sum = warp_sum(sum);
+  __syncthreads();
+  if ((tid & 31) == 0) s_red[tid >> 5] = sum;
+  __syncthreads();
+  sum = 0.f;
+  for (int j = 0; j < DIM / 32; ++j) sum += s_red[j];
+
+  const int grp = tid / L, l = tid % L;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* po = reinterpret_cast<const float4*>(a.po + slot * DIM) + l;
+#pragma unroll 8
+  for (int j = grp; j < chunks; j += 4) {
+    const float4 x = __ldcg(po + j * step * L);
+    const float wt = s_wt[j];
+    if (wt != -1.f) {
+      o.x = fmaf(wt, x.x, o.x);
+      o.y = fmaf(wt, x.y, o.y);
+      o.z = fmaf(wt, x.z, o.z);
+      o.w = fmaf(wt, x.w, o.w);
+    }
+  }
+  s_o[grp][l] = o;
+  __syncthreads();
+  if (grp == 0) {
+    const float4 p = s_o[1][l], q = s_o[2][l], r = s_o[3][l];
+    const float inv = sum > 0.f || sum != sum ? __frcp_rn(sum) : 0.f;
+    const float x = ((o.x + p.x) + (q.x + r.x)) * inv, y = ((o.y + p.y) + (q.y + r.y)) * inv;
+    const float z = ((o.z + p.z) + (q.z + r.z)) * inv, u = ((o.w + p.w) + (q.w + r.w)) * inv;
+    uint8_t* dst = static_cast<uint8_t*>(a.out) + ((long long)(s0.x + node) * a.out_stride + qh * DIM + 4 * l) * 2;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(x, y), pack2<BF16>(z, u));
+    if (l == 0 && a.lse)
+      a.lse[(long long)(s0.x + node) * (a.Hkv * a.G) + qh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  }
+}
+
+// --------------------------------------------------------------------- host --
+
+namespace {
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+struct TaDevice {
+  int sms = 0;
+  bool ready = false;
+};
+std::mutex g_ta_mu;
+TaDevice g_ta[64];
+EncodeFn g_encode = nullptr;
+
+template <int DIM, bool BF16>
+cudaError_t ta_attributes() {
+  return cudaFuncSetAttribute(tree_attn_kernel<DIM, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, TaShape<DIM>::SMEM);
+}
+
+// SM count and kernel attributes of the current device; the driver's encoder.
+cudaError_t ta_device(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(g_ta_mu);
+  TaDevice& d = g_ta[dev];
+  if (!g_encode) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if ((e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q)) != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<EncodeFn>(f);
+  }
+  if (!d.ready) {
+    if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if ((e = ta_attributes<64, false>()) != cudaSuccess || (e = ta_attributes<64, true>()) != cudaSuccess ||
+        (e = ta_attributes<128, false>()) != cudaSuccess || (e = ta_attributes<128, true>()) != cudaSuccess ||
+        (e = ta_attributes<256, false>()) != cudaSuccess || (e = ta_attributes<256, true>()) != cudaSuccess)
+      return e;
+    d.ready = true;
+  }
+  *sms = std::min(d.sms, 256);
+  return cudaSuccess;
+}
+
+// A map of rank 5 whose innermost axis is the 64 elements of a 128-byte chunk;
+// strides (of the other four axes) in elements.
+bool encode(CUtensorMap* m, bool bf16, const void* base, const long long (&dims)[4], const long long (&strides)[4],
+            const int (&box)[4]) {
+  cuuint64_t gd[5] = {64, 0, 0, 0, 0}, gs[4];
+  cuuint32_t bx[5] = {64, 0, 0, 0, 0}, es[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    gd[i + 1] = (cuuint64_t)dims[i];
+    gs[i] = (cuuint64_t)strides[i] * 2;
+    bx[i + 1] = (cuuint32_t)box[i];
+  }
+  return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(base), gd, gs, bx,
+                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The two M tilings of G query heads x up to max_nodes tokens: all heads of a
+// token together (trees that fit one tile), and for larger trees the heads per
+// tile that need the fewest tiles at max_nodes (64 tokens x 6 heads: 2 heads x 64
+// tokens in 3 tiles, where whole tokens would take 4).
+void ta_tilings(int G, int max_nodes, TaTiling (&t)[2]) {
+  auto make = [&](int gb) { return TaTiling{gb, std::min(kTaRows / gb, max_nodes), (G + gb - 1) / gb}; };
+  t[0] = make(G);
+  t[1] = t[0];
+  auto tiles = [&](const TaTiling& x) { return x.ng * ((max_nodes + x.nb - 1) / x.nb); };
+  for (int gb = G - 1; gb >= 1; --gb)
+    if (tiles(make(gb)) < tiles(t[1])) t[1] = make(gb);
+}
+
+struct TaLayout {
+  size_t seqs, items, pml, po, total;
+};
+
+TaLayout ta_layout(const TaTiling (&t)[2], int dim, int Hkv, int G, int n_batch, int max_nodes, int grid) {
+  const long long nm = std::max(1, t[1].ng * ((max_nodes + t[1].nb - 1) / t[1].nb));
+  const long long items = (long long)n_batch * Hkv * nm + (long long)grid * kTaWaves;
+  const long long rows = (long long)grid * kTaSplitItems * std::min(kTaRows, max_nodes * G);
+  TaLayout l;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  l.seqs = 256;
+  l.items = l.seqs + up(sizeof(TaSeq) * (size_t)n_batch);
+  l.pml = l.items + up(16 * (size_t)items);
+  l.po = l.pml + up(8 * (size_t)rows);
+  l.total = l.po + up(4 * (size_t)rows * dim);
+  return l;
+}
+
+// Shape checks shared by the call and its workspace query.
+int ta_check(const char* me, const qhl_kv_pages* kv, int Hq, int n_rows, int n_batch, int max_nodes) {
+  const int rc = check_pages(me, kv);
+  if (rc) return rc;
+  if (Hq < 1 || Hq % kv->kv_heads || Hq / kv->kv_heads > kTaRows)
+    return verify_err(me, STAGE_E_ARG, "n_q_heads must be a multiple of kv_heads, at most 128 of them each");
+  if (n_rows < 0 || n_batch < 1 || n_batch > kMaxBatch || max_nodes < 1 || max_nodes > kMaxNodes)
+    return verify_err(me, STAGE_E_ARG, "n_rows, n_batch (1..2048) or max_nodes (1..128) out of range");
+  if ((long long)n_batch * kv->kv_heads * (Hq / kv->kv_heads) * max_nodes > 1LL << 26)
+    return verify_err(me, STAGE_E_ARG, "too many query rows");
+  return 0;
+}
+
+template <int DIM, bool BF16>
+cudaError_t ta_launch(const TaArgs& a, int Hq, cudaStream_t s) {
+  cudaError_t e = launch_ex(tree_plan_kernel<DIM>, dim3(1), dim3(512), 0, s, false, a);
+  if (e == cudaSuccess) e = launch_ex(tree_attn_kernel<DIM, BF16>, dim3(a.grid), dim3(kTaThreads), TaShape<DIM>::SMEM, s, true, a);
+  if (e == cudaSuccess) e = launch_ex(tree_join_kernel<DIM, BF16>, dim3(Hq, a.max_nodes, a.n_batch), dim3(DIM), 0, s, true, a);
+  return e;
+}
+
+}  // namespace
+
+}  // namespace qhl
+
+using namespace qhl;
+
+extern "C" {
+
+size_t qhl_tree_attention_workspace(const qhl_kv_pages* kv, int n_q_heads, int n_rows, int n_batch, int max_nodes) {
+  const char* me = "qhl_tree_attention_workspace";
+  if (ta_check(me, kv, n_q_heads, n_rows, n_batch, max_nodes)) return 0;
+  int sms = 0;
+  const cudaError_t e = ta_device(&sms);
+  if (e != cudaSuccess) {
+    verify_cuda_err(me, e);
+    return 0;
+  }
+  const int G = n_q_heads / kv->kv_heads;
+  TaTiling t[2];
+  ta_tilings(G, max_nodes, t);
+  return ta_layout(t, kv->dim, kv->kv_heads, G, n_batch, max_nodes, sms).total;
+}
+
+int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_rows, int n_batch, int max_nodes,
+                       const int* seq_dev, const int* q_start_dev, const int* parent_dev, const void* q_dev,
+                       long long q_stride, const void* k_new_dev, const void* v_new_dev, long long new_stride,
+                       void* out_dev, long long out_stride, float* lse_dev, float scale, void* workspace_dev,
+                       size_t workspace_bytes, void* stream) {
+  const char* me = "qhl_tree_attention";
+  int rc = ta_check(me, kv, n_q_heads, n_rows, n_batch, max_nodes);
+  if (rc) return rc;
+  if (!seq_dev || !q_start_dev || !parent_dev || !q_dev || !k_new_dev || !v_new_dev || !out_dev || !workspace_dev)
+    return verify_err(me, STAGE_E_ARG, "null pointer");
+  if (layer < 0 || layer >= kv->n_layers) return verify_err(me, STAGE_E_ARG, "layer out of range");
+  if (!(scale > 0) || !std::isfinite(scale)) return verify_err(me, STAGE_E_ARG, "scale must be positive");
+  const long long qw = (long long)n_q_heads * kv->dim, kw = (long long)kv->kv_heads * kv->dim, most = 1LL << 38;
+  if (!aligned16(q_dev) || !aligned16(k_new_dev) || !aligned16(v_new_dev) || !aligned16(out_dev) || !aligned16(workspace_dev) ||
+      q_stride % 8 || new_stride % 8 || out_stride % 8)
+    return verify_err(me, STAGE_E_ARG, "bases must be 16-byte aligned and strides multiples of 8");
+  if (q_stride < qw || out_stride < qw || new_stride < kw || q_stride > most || new_stride > most || out_stride > most)
+    return verify_err(me, STAGE_E_ARG, "a row stride is shorter than its heads, or too long");
+  if (n_rows == 0) return 0;
+
+  TaArgs a = {};
+  cudaError_t e = ta_device(&a.grid);
+  if (e == cudaSuccess) e = verify_error_word(&a.err);
+  if (e != cudaSuccess) return verify_cuda_err(me, e);
+  const int dim = kv->dim, G = n_q_heads / kv->kv_heads, KT = dim == 256 ? 64 : 128, CH = dim / 64, P = kv->page_rows;
+  const bool bf16 = kv->dtype == QHL_BF16;
+  ta_tilings(G, max_nodes, a.tiling);
+  const TaLayout l = ta_layout(a.tiling, dim, kv->kv_heads, G, n_batch, max_nodes, a.grid);
+  if (workspace_bytes < l.total)
+    return verify_err(me, STAGE_E_ARG, "the workspace needs " + std::to_string(l.total) + " bytes");
+  a.box = std::min(P, KT);
+  a.dbox = std::min(KT, (max_nodes + 7) / 8 * 8);
+  const uint16_t* kb = static_cast<const uint16_t*>(kv->k_dev) + (long long)layer * kv->stride_layer;
+  const uint16_t* vb = static_cast<const uint16_t*>(kv->v_dev) + (long long)layer * kv->stride_layer;
+  const long long pd[4] = {P, CH, kv->kv_heads, kv->n_pages}, ps[4] = {kv->stride_row, 64, kv->stride_head, kv->stride_page};
+  const int pb[4] = {a.box, a.box == KT ? CH : 1, 1, 1};
+  const long long nd[4] = {n_rows, CH, kv->kv_heads, 1}, ns[4] = {new_stride, 64, dim, 64};
+  const int nb[4] = {a.dbox, a.dbox == KT ? CH : 1, 1, 1};
+  const long long qd[4] = {G, n_rows, CH, kv->kv_heads}, qs[4] = {dim, q_stride, 64, (long long)G * dim};
+  bool fine = encode(&a.k, bf16, kb, pd, ps, pb) && encode(&a.v, bf16, vb, pd, ps, pb) && encode(&a.kn, bf16, k_new_dev, nd, ns, nb) &&
+              encode(&a.vn, bf16, v_new_dev, nd, ns, nb);
+  for (int i = 0; i < 2; ++i) {
+    const int qb[4] = {a.tiling[i].gb, a.tiling[i].nb, 1, 1};
+    fine = fine && encode(&a.q[i], bf16, q_dev, qd, qs, qb);
+  }
+  if (!fine) return verify_err(me, STAGE_E_UNSUPPORTED, "the driver refused a tensor map for these strides");
+  a.page_rows = P;
+  a.n_pages = kv->n_pages;
+  a.max_pages = kv->max_pages;
+  a.n_seqs = kv->n_seqs;
+  a.Hkv = kv->kv_heads;
+  a.G = G;
+  a.n_rows = n_rows;
+  a.n_batch = n_batch;
+  a.max_nodes = max_nodes;
+  a.table = kv->table_dev;
+  a.len = kv->len_dev;
+  a.seq = seq_dev;
+  a.q_start = q_start_dev;
+  a.parent = parent_dev;
+  a.v_new = v_new_dev;
+  a.new_stride = new_stride;
+  a.out = out_dev;
+  a.out_stride = out_stride;
+  a.lse = lse_dev;
+  a.c = scale * 1.44269504088896340736f;
+  uint8_t* ws = static_cast<uint8_t*>(workspace_dev);
+  a.hdr = reinterpret_cast<int*>(ws);
+  a.seqs = reinterpret_cast<TaSeq*>(ws + l.seqs);
+  a.items = reinterpret_cast<int4*>(ws + l.items);
+  a.pml = reinterpret_cast<float2*>(ws + l.pml);
+  a.po = reinterpret_cast<float*>(ws + l.po);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dim == 256)
+    e = bf16 ? ta_launch<256, true>(a, n_q_heads, s) : ta_launch<256, false>(a, n_q_heads, s);
+  else if (dim == 128)
+    e = bf16 ? ta_launch<128, true>(a, n_q_heads, s) : ta_launch<128, false>(a, n_q_heads, s);
+  else
+    e = bf16 ? ta_launch<64, true>(a, n_q_heads, s) : ta_launch<64, false>(a, n_q_heads, s);
+  return e == cudaSuccess ? 0 : verify_cuda_err(me, e);
+}
+
+}  // extern "C"
