@@ -55,9 +55,10 @@ struct TaShape {
   static constexpr int KT = DIM == 256 ? 64 : 128;     // keys per tile
   static constexpr int CH = DIM / 64;                  // 128-byte chunks of a row
   static constexpr int SLOT = KT * DIM * 2;            // bytes of a ring slot
-  static constexpr int NS = DIM == 256 ? 4 : DIM == 128 ? 5 : 8;
-  static constexpr int QB = kTaRows * DIM * 2;
-  static constexpr int SMEM = 1024 + QB + NS * SLOT;   // 1024: room to align the swizzle atoms
+  static constexpr int NS = DIM == 64 ? 12 : 6;        // 192 KB in flight or in use
+  static constexpr int SMEM = 1024 + NS * SLOT;        // 1024: room to align the swizzle atoms
+  // tensor-memory columns: O, Q (two elements a column), S of even and odd tiles
+  static constexpr uint32_t S0 = 256, Q0 = DIM == 256 ? 384 : DIM;
 };
 
 // One tree as the plan sees it.
@@ -65,28 +66,24 @@ struct TaSeq {
   int row0, n, seq, ctx;
   int chunks;        // ranges its key tiles are split into
   int slot0;         // its first partial row
-  int wide;          // which of the two M tilings
   int tiles;
-};
-
-// An M tiling: gb query heads x nb tokens of one KV head.
-struct TaTiling {
-  int gb, nb, ng;    // ng = ceil(G / gb)
+  int pad;
 };
 
 struct TaArgs {
-  CUtensorMap q[2];            // per tiling
   CUtensorMap k, v;            // cache pages
   CUtensorMap kn, vn;          // drafted rows
-  TaTiling tiling[2];
   int box, dbox;               // rows per TMA box of a page / of drafted rows
-  int page_rows, n_pages, max_pages, n_seqs;
+  int box_shift, page_shift;   // log2 of box and of the rows of a page
+  int n_pages, max_pages, n_seqs;
   int Hkv, G, n_rows, n_batch, max_nodes;
   const int* table;
   const int* len;
   const int* seq;
   const int* q_start;
   const int* parent;
+  const void* q;
+  long long q_stride;
   const void* v_new;
   long long new_stride;
   void* out;
@@ -124,16 +121,14 @@ __global__ void __launch_bounds__(512) tree_plan_kernel(const __grid_constant__ 
       s.seq = 0;
     } else {
       s.ctx = a.len[s.seq];
-      if (s.ctx < 0 || s.ctx > (long long)a.max_pages * a.page_rows) {
+      if (s.ctx < 0 || s.ctx > ((long long)a.max_pages << a.page_shift)) {
         atomicOr(a.err, ERR_BAD_INDEX);
         s.ctx = 0;
       }
     }
-    s.wide = s.n > a.tiling[0].nb;
     s.tiles = s.n ? (s.ctx + KT - 1) / KT + (s.n + KT - 1) / KT : 0;
-    s.chunks = s.slot0 = 0;
-    const TaTiling t = a.tiling[s.wide];
-    const int nm = s.n ? t.ng * ((s.n + t.nb - 1) / t.nb) : 0;
+    s.chunks = s.slot0 = s.pad = 0;
+    const int nm = (s.n * a.G + kTaRows - 1) / kTaRows;
     a.seqs[b] = s;
     s_nt[b] = s.tiles;
     s_nm[b] = nm * a.Hkv;
@@ -268,14 +263,14 @@ QHL_DEV float widen16(uint32_t h) {
 // and at an item's end; pv_done is kept per tile parity for them: when S of tile
 // T is there, the product of tile T - 2, issued before it, is complete.
 struct TaBars {
-  uint64_t full[8], empty[8], vok[8];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2], pv_done[2], mask_full, mask_empty;
+  uint64_t full[12], empty[12], vok[12];
+  uint64_t q_ready, s_full[2], p_ready[2], pv_done[2], mask_full, mask_empty;
 };
 
 // What the roles know of an item.
 struct TaItem {
   TaSeq s;
-  int t0, t1, h, ck, n0, g0, nct;   // n0, g0: the M tile's first token and query head; nct: cache tiles
+  int t0, t1, h, ck, mt, nct;   // nct: cache tiles
 };
 
 template <int DIM>
@@ -289,19 +284,21 @@ QHL_DEV TaItem ta_item(const TaArgs& a, int i) {
   r.t1 = it.z;
   r.h = it.w & 255;
   r.ck = it.w >> 16;
-  const int mt = it.w >> 8 & 255;
-  const TaTiling& t = a.tiling[r.s.wide];
-  r.g0 = mt % t.ng * t.gb;
-  r.n0 = mt / t.ng * t.nb;
+  r.mt = it.w >> 8 & 255;
   r.nct = (r.s.ctx + TaShape<DIM>::KT - 1) / TaShape<DIM>::KT;
   return r;
+}
+
+// Rows of V that the product of a tile needs: its keys, up to a multiple of 16.
+template <int KT>
+QHL_DEV int ta_keys(const TaItem& w, int tile) {
+  return tile >= w.nct ? min(KT, w.s.n - (tile - w.nct) * KT) : min(KT, w.s.ctx - tile * KT);
 }
 
 template <int DIM, bool BF16>
 __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_constant__ TaArgs a) {
   using Sh = TaShape<DIM>;
   constexpr int KT = Sh::KT, CH = Sh::CH, NS = Sh::NS, HK = KT / 2;
-  constexpr uint32_t kS0 = 256;                      // tensor-memory columns: O at 0, S at 256 and 256 + KT
   extern __shared__ uint8_t smem_raw[];
   __shared__ TaBars bars;
   __shared__ uint32_t s_tmem;
@@ -311,7 +308,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
   __shared__ float s_max[2][2][kTaRows], s_sum[2][kTaRows];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t sq = (smem_u32(smem_raw) + 1023u) & ~1023u, ring = sq + Sh::QB;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   auto bar = [](const uint64_t& b) { return smem_u32(&b); };
 
   if (tid == 0) {
@@ -319,16 +316,15 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
     for (int i = 0; i < NS; ++i) {
       mbar_init(bar(bars.full[i]), 1);
       mbar_init(bar(bars.empty[i]), 1);
-      mbar_init(bar(bars.vok[i]), 2);
+      mbar_init(bar(bars.vok[i]), 1);
     }
-    mbar_init(bar(bars.q_full), 1);
-    mbar_init(bar(bars.q_empty), 1);
+    mbar_init(bar(bars.q_ready), 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(bars.s_full[i]), 1);
       mbar_init(bar(bars.p_ready[i]), 8);
       mbar_init(bar(bars.pv_done[i]), 1);
     }
-    mbar_init(bar(bars.mask_full), 2);
+    mbar_init(bar(bars.mask_full), 1);
     mbar_init(bar(bars.mask_empty), 8);
     fence_mbar_init();
   }
@@ -338,7 +334,6 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
     tma_prefetch_map(&a.v);
     tma_prefetch_map(&a.kn);
     tma_prefetch_map(&a.vn);
-    tma_prefetch_map(&a.q[0]);
   }
   __syncthreads();
   tc_fence_after();
@@ -354,25 +349,21 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
 
   if (warp == 8) {
     // ---------------------------------------------------------------- TMA --
-    uint32_t r = 0, it = 0;
-    auto acquire = [&](uint32_t bytes) {             // the next slot, once its last contents are used
-      const uint32_t s = r % NS, ph = r / NS & 1;
-      ok = wait_warp(bars.empty[s], ph ^ 1);
-      if (lane == 0 && ok) mbar_arrive_expect_tx(bar(bars.full[s]), bytes);
-      ++r;
-      return s;
-    };
-    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x, ++it) {
+    // A copy per (box of rows, chunk) where a box is less than a tile, so that the
+    // chunks of all boxes are KT rows apart in the slot; the lanes issue them
+    // together.
+    uint32_t r = 0;
+    const int pchunks = a.box == KT ? 1 : CH, dchunks = a.dbox == KT ? 1 : CH;
+    const int pbox = lane / pchunks, pchunk = lane % pchunks, boxes_per_tile = KT >> a.box_shift;
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
       const TaItem w = ta_item<DIM>(a, i);
-      const TaTiling& t = a.tiling[w.s.wide];
       const int* row = a.table + (size_t)w.s.seq * a.max_pages;
       // page numbers of this item's boxes, 32 at a time, one batch ahead
-      const int boxes_per_tile = KT / a.box, box_end = (w.s.ctx + a.box - 1) / a.box;
-      int jb = w.t0 * boxes_per_tile;
+      const int box_end = (w.s.ctx + a.box - 1) >> a.box_shift;
       auto page_of = [&](int j) {
         int pg = -1;
         if (j < box_end) {
-          pg = __ldg(row + (int)((long long)j * a.box / a.page_rows));
+          pg = __ldg(row + (j >> (a.page_shift - a.box_shift)));
           if (pg < 0 || pg >= a.n_pages) {
             atomicOr(a.err, ERR_BAD_INDEX);
             pg = a.n_pages;                          // beyond the tensor: the copy fills zeros
@@ -380,137 +371,122 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
         }
         return pg;
       };
-      int ids = page_of(jb + lane), ids_next = page_of(jb + 32 + lane), ids_at = jb;
-
-      if (!(ok = wait_warp(bars.q_empty, (it & 1) ^ 1))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(bars.q_full), CH * t.gb * t.nb * 128);
-        for (int c = 0; c < CH; ++c)
-          tma_load_5d(sq + c * kTaRows * 128, &a.q[w.s.wide], bar(bars.q_full), w.g0, w.s.row0 + w.n0, c, w.h);
-      }
+      int ids_at = w.t0 * boxes_per_tile, ids = page_of(ids_at + lane), ids_next = page_of(ids_at + 32 + lane);
       for (int tile = w.t0; ok && tile < w.t1; ++tile) {
-        if (tile < w.nct) {
-          const int nb = min(boxes_per_tile, box_end - tile * boxes_per_tile);
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            const uint32_t s = acquire((uint32_t)nb * a.box * DIM * 2);
-            if (!ok) break;
-            const uint32_t dst = ring + s * Sh::SLOT;
-            const CUtensorMap* map = kv ? &a.v : &a.k;
-            for (int j = 0; j < nb; ++j) {
-              const int jj = tile * boxes_per_tile + j;
-              if (jj - ids_at >= 32) {               // tiles never straddle a batch: 32 is a multiple of their boxes
-                ids = ids_next;
-                ids_at += 32;
-                ids_next = page_of(ids_at + 32 + lane);
-              }
-              const int pg = __shfl_sync(0xffffffffu, ids, jj - ids_at);
-              if (lane == 0) {
-                const int rr = (int)((long long)jj * a.box % a.page_rows);
-                if (a.box == KT) {
-                  tma_load_5d(dst, map, bar(bars.full[s]), rr, 0, w.h, pg);
-                } else {
-                  for (int c = 0; c < CH; ++c)
-                    tma_load_5d(dst + c * KT * 128 + j * a.box * 128, map, bar(bars.full[s]), rr, c, w.h, pg);
-                }
-              }
-            }
+        const bool draft = tile >= w.nct;
+        const int b0 = tile * boxes_per_tile;
+        int nb = 1, pg = 0, rr = w.s.row0 + (tile - w.nct) * KT;
+        if (!draft) {
+          nb = min(boxes_per_tile, box_end - b0);
+          if (b0 - ids_at >= 32) {                   // 32 is a multiple of a tile's boxes
+            ids = ids_next;
+            ids_at += 32;
+            ids_next = page_of(ids_at + 32 + lane);
           }
-        } else {
-          const int rr = w.s.row0 + (tile - w.nct) * KT;
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            const uint32_t s = acquire((uint32_t)a.dbox * DIM * 2);
-            if (!ok || lane) continue;
-            const uint32_t dst = ring + s * Sh::SLOT;
-            const CUtensorMap* map = kv ? &a.vn : &a.kn;
-            if (a.dbox == KT) {
-              tma_load_5d(dst, map, bar(bars.full[s]), rr, 0, w.h, 0);
-            } else {
-              for (int c = 0; c < CH; ++c) tma_load_5d(dst + c * KT * 128, map, bar(bars.full[s]), rr, c, w.h, 0);
-            }
-          }
+          pg = __shfl_sync(0xffffffffu, ids, (b0 - ids_at + pbox) & 31);
+          rr = (b0 + pbox) << a.box_shift & ((1 << a.page_shift) - 1);
+        }
+        const int copies = draft ? dchunks : nb * pchunks;
+        const uint32_t bytes = (uint32_t)(draft ? a.dbox : nb << a.box_shift) * DIM * 2;
+        const int c = draft ? lane : pchunk;
+        const uint32_t off = (draft ? 0u : (uint32_t)(pbox << a.box_shift) * 128u) + (uint32_t)c * (KT * 128);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t s = r % NS, ph = r / NS & 1;
+          ++r;
+          ok = wait_warp(bars.empty[s], ph ^ 1);     // its last contents are used
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(bars.full[s]), bytes);
+          __syncwarp();
+          if (lane < copies)
+            tma_load_5d(ring + s * Sh::SLOT + off, draft ? (kv ? &a.vn : &a.kn) : (kv ? &a.v : &a.k), bar(bars.full[s]), rr, c, w.h, pg);
         }
       }
     }
   } else if (warp == 9) {
-    // ---------------------------------------------------------------- MMA --
+    // ---------------------------------------------------------- S = Q K^T --
+    // The two products have an issuer each: a wait that is over still takes some
+    // 250 cycles under load, and one thread's waits for both left the tensor core
+    // idle for 40% of a tile (2400 cycles instead of 1450 at 256 dimensions).
     if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_f16(BF16, false, kTaRows, KT), id_pv = idesc_f16(BF16, true, kTaRows, DIM);
-      uint32_t r = 0, T = 0, it = 0, vok_phase = 0;
-      bool have = false, p_first = false, p_care = false;
-      uint32_t p_T = 0, p_r = 0;
-      auto pv = [&]() {                              // the product with V of the tile before
-        const uint32_t b = p_T & 1, s = p_r % NS;
-        if (!mbar_wait(bar(bars.p_ready[b]), p_T >> 1 & 1, a.err, kTaWait)) return false;
-        if (!mbar_wait(bar(bars.full[s]), p_r / NS & 1, a.err, kTaWait)) return false;
-        if (p_care) {
-          if (!mbar_wait(bar(bars.vok[s]), vok_phase >> s & 1, a.err, kTaWait)) return false;
-          vok_phase ^= 1u << s;
-        }
-        tc_fence_after();
-        const uint32_t p = tmem + kS0 + b * KT;
-        const uint64_t vd = smem_desc_sw128(ring + s * Sh::SLOT, KT * 128);
-#pragma unroll
-        for (int k = 0; k < KT / 16; ++k) mma_f16_ts(tmem, p + k * 8, vd + (uint64_t)(k * 2048 >> 4), id_pv, !p_first || k);
-        tc_commit(&bars.empty[s]);
-        tc_commit(&bars.pv_done[b]);
-        return true;
-      };
+      constexpr uint32_t id = idesc_f16(BF16, false, kTaRows, KT);
+      uint32_t r = 0, T = 0, it = 0;
       for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x, ++it) {
-        const TaItem w = ta_item<DIM>(a, i);
-        if (!(ok = mbar_wait(bar(bars.q_full), it & 1, a.err, kTaWait))) break;
-        for (int tile = w.t0; tile < w.t1; ++tile, ++T, r += 2) {
+        const int4 w = __ldcg(a.items + i);
+        if (!(ok = mbar_wait(bar(bars.q_ready), it & 1, a.err, kTaWait))) break;
+        for (int tile = w.y; tile < w.z; ++tile, ++T, r += 2) {
           const uint32_t s = r % NS, b = T & 1;
           if (!(ok = mbar_wait(bar(bars.full[s]), r / NS & 1, a.err, kTaWait))) break;
+          // p of the tile before last, which lies in this S, is used
+          if (T >= 2 && !(ok = mbar_wait(bar(bars.pv_done[b]), (T >> 1 & 1) ^ 1, a.err, kTaWait))) break;
           tc_fence_after();
-          const uint64_t qd = smem_desc_sw128(sq, 16), kd = smem_desc_sw128(ring + s * Sh::SLOT, 16);
+          const uint64_t kd = smem_desc_sw128(ring + s * Sh::SLOT, 16);
 #pragma unroll
           for (int k = 0; k < DIM / 16; ++k)
-            mma_f16_ss(tmem + kS0 + b * KT, qd + (uint64_t)((k / 4) * (kTaRows * 128) + (k % 4) * 32 >> 4),
-                       kd + (uint64_t)((k / 4) * (KT * 128) + (k % 4) * 32 >> 4), id_qk, k != 0);
+            mma_f16_ts(tmem + Sh::S0 + b * KT, tmem + Sh::Q0 + k * 8, kd + (uint64_t)((k / 4) * (KT * 128) + (k % 4) * 32 >> 4), id, k != 0);
           tc_commit(&bars.s_full[b]);
           tc_commit(&bars.empty[s]);
-          if (tile == w.t1 - 1) tc_commit(&bars.q_empty);
-          if (have && !(ok = pv())) break;
-          have = true;
-          p_T = T;
-          p_r = r + 1;
-          p_first = tile == w.t0;
-          p_care = tile >= w.nct || (tile + 1) * KT > w.s.ctx;
         }
       }
-      if (ok && have) pv();
     }
     __syncwarp();
-  } else if (warp >= 10) {
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ O += p V --
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_f16(BF16, true, kTaRows, DIM);
+      uint32_t r = 1, T = 0, vok_phase = 0;
+      for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+        const TaItem w = ta_item<DIM>(a, i);
+        for (int tile = w.t0; tile < w.t1; ++tile, ++T, r += 2) {
+          const uint32_t s = r % NS, b = T & 1;
+          const int keys = ta_keys<KT>(w, tile);
+          if (!(ok = mbar_wait(bar(bars.full[s]), r / NS & 1, a.err, kTaWait))) break;
+          if (tile >= w.nct || keys < KT) {
+            if (!(ok = mbar_wait(bar(bars.vok[s]), vok_phase >> s & 1, a.err, kTaWait))) break;
+            vok_phase ^= 1u << s;
+          }
+          if (!(ok = mbar_wait(bar(bars.p_ready[b]), T >> 1 & 1, a.err, kTaWait))) break;
+          tc_fence_after();
+          const uint32_t p = tmem + Sh::S0 + b * KT;
+          const uint64_t vd = smem_desc_sw128(ring + s * Sh::SLOT, KT * 128);
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k)
+            if (16 * k < keys) mma_f16_ts(tmem, p + k * 8, vd + (uint64_t)(k * 2048 >> 4), id, tile != w.t0 || k);
+          tc_commit(&bars.pv_done[b]);
+          tc_commit(&bars.empty[s]);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 11) {
     // ------------------------------------------- masks, tiles that need care --
-    const int ft = tid - 320;                        // 0..63
-    uint32_t r = 0, it = 0;
-    for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++it) {
+    uint32_t r = 1, it = 0;
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x, ++it) {
       const TaItem w = ta_item<DIM>(a, i);
       const int n = w.s.n;
-      if (ok && it) ok = wait_warp(bars.mask_empty, (it - 1) & 1);
-      if (!(ok = bar_and(6, 64, ok))) break;
-      if (ft < 4) s_bad[ft] = 0;
+      if (it && !(ok = wait_warp(bars.mask_empty, (it - 1) & 1))) break;
+      if (lane < 4) s_bad[lane] = 0;
       // ancestors by doubling: after k rounds those up to 2^k steps away; a jump
       // ends at -1 (the cached sequence) or -2 (padded: nothing is seen)
-      for (int x = ft; x < n; x += 64) {
+      for (int x = lane; x < n; x += 32) {
         int p = __ldg(a.parent + w.s.row0 + x);
         if (p < -2 || p >= x) {
           atomicOr(a.err, ERR_BAD_INDEX);
           p = -2;
         }
         s_jump[x] = p;
-        uint32_t m[4] = {0, 0, 0, 0};
-        m[x >> 5] = 1u << (x & 31);
+        uint32_t m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = x >> 5 == j ? 1u << (x & 31) : 0u;
         s_anc[x] = make_uint4(m[0], m[1], m[2], m[3]);
       }
-      named_sync(6, 64);
+      __syncwarp();
       for (int step = 1; step < n; step <<= 1) {
-        uint4 m[2];
-        int jp[2];
+        uint4 m[4];
+        int jp[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int x = ft + 64 * u;
+        for (int u = 0; u < 4; ++u) {
+          const int x = lane + 32 * u;
           jp[u] = -1;
           if (x < n) {
             m[u] = s_anc[x];
@@ -522,16 +498,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
             }
           }
         }
-        named_sync(6, 64);
+        __syncwarp();
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (ft + 64 * u < n) {
-            s_anc[ft + 64 * u] = m[u];
-            s_jump[ft + 64 * u] = jp[u];
+        for (int u = 0; u < 4; ++u)
+          if (lane + 32 * u < n) {
+            s_anc[lane + 32 * u] = m[u];
+            s_jump[lane + 32 * u] = jp[u];
           }
-        named_sync(6, 64);
+        __syncwarp();
       }
-      for (int x = ft; x < n; x += 64)
+      for (int x = lane; x < n; x += 32)
         if (s_jump[x] == -2) s_anc[x] = make_uint4(0, 0, 0, 0);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars.mask_full));
@@ -539,20 +515,20 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
       for (int tile = w.t0; ok && tile < w.t1; ++tile, r += 2) {
         // every tile's V is waited for, so that the wait's parity is that of its phase
         const bool draft = tile >= w.nct;
-        const uint32_t s = (r + 1) % NS;
-        if (!(ok = wait_warp(bars.full[s], (r + 1) / NS & 1))) break;
-        if (!draft && (tile + 1) * KT <= w.s.ctx) continue;
-        const int dt = tile - w.nct;
-        const int valid = draft ? min(KT, n - dt * KT) : w.s.ctx - tile * KT;
+        const uint32_t s = r % NS;
+        const int keys = ta_keys<KT>(w, tile);
+        if (!(ok = wait_warp(bars.full[s], r / NS & 1))) break;
+        if (!draft && keys == KT) continue;
         uint8_t* base = smem_raw + (ring + s * Sh::SLOT - smem_u32(smem_raw));
-        // units of 16 bytes; the swizzle permutes units within a row only
-        for (int u = ft; u < CH * KT * 8; u += 64) {
-          const int rr = u / 8 % KT;
-          uint4* p = reinterpret_cast<uint4*>(base) + u;
-          if (rr >= valid) {
-            *p = make_uint4(0, 0, 0, 0);
-          } else if (draft) {
-            uint4 x = *p;
+        // Rows up to the multiple of 16 that the product reads.  Units of 16 bytes;
+        // the swizzle permutes the units of a row only.
+        const int end = (keys + 15) & ~15, begin = draft ? 0 : keys;
+#pragma unroll 1
+        for (int ch = 0; ch < CH; ++ch) {
+          uint4* p = reinterpret_cast<uint4*>(base + ch * (KT * 128));
+#pragma unroll 4
+          for (int u = begin * 8 + lane; u < keys * 8; u += 32) {
+            uint4 x = p[u];
             uint32_t* y = reinterpret_cast<uint32_t*>(&x);
             bool bad = false;
 #pragma unroll
@@ -561,11 +537,12 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
               if (non_finite16<BF16>(y[e] >> 16)) { y[e] &= 0xffffu; bad = true; }
             }
             if (bad) {
-              *p = x;
-              const int node = dt * KT + rr;
+              p[u] = x;
+              const int node = (tile - w.nct) * KT + u / 8;
               atomicOr(&s_bad[node >> 5], 1u << (node & 31));
             }
           }
+          for (int u = keys * 8 + lane; u < end * 8; u += 32) p[u] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -580,10 +557,25 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
     uint32_t T = 0, it = 0;
     for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++it) {
       const TaItem w = ta_item<DIM>(a, i);
-      const TaTiling& t = a.tiling[w.s.wide];
-      const int nl = row / t.gb, gl = row - nl * t.gb, node = w.n0 + nl, g = w.g0 + gl;
-      const bool valid = nl < t.nb && node < w.s.n && g < a.G;
+      const int qr = w.mt * kTaRows + row, node = qr / a.G, g = qr - node * a.G;   // the thread's token and query head
+      const bool valid = node < w.s.n;
       const bool active = __any_sync(0xffffffffu, valid);
+      // Q to tensor memory: the tile's last S is complete, so nothing reads it now
+      if (active) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (long long)(w.s.row0 + node) * a.q_stride +
+                                                          (w.h * a.G + g) * DIM + hf * (DIM / 2));
+#pragma unroll
+        for (int j = 0; j < DIM / 64; ++j) {         // 32 elements, 16 columns
+          uint4 x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = valid ? __ldg(src + 4 * j + e) : make_uint4(0, 0, 0, 0);
+          tmem_st16(tmem + lanes + Sh::Q0 + hf * (DIM / 4) + 16 * j, reinterpret_cast<const uint32_t*>(x));
+        }
+        tmem_st_wait();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.q_ready));
       ok = wait_warp(bars.mask_full, it & 1);
       uint4 anc = make_uint4(0, 0, 0, 0);
       if (valid) anc = s_anc[node];
@@ -600,7 +592,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
         }
         if (active) {
           tc_fence_after();
-          const uint32_t sb = tmem + lanes + kS0 + b * KT;
+          const uint32_t sb = tmem + lanes + Sh::S0 + b * KT;
           uint32_t sv[HK / 32][32];
 #pragma unroll
           for (int j = 0; j < HK / 32; ++j) tmem_ld32(sb + hf * HK + 32 * j, sv[j]);
@@ -903,25 +895,12 @@ bool encode(CUtensorMap* m, bool bf16, const void* base, const long long (&dims)
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The two M tilings of G query heads x up to max_nodes tokens: all heads of a
-// token together (trees that fit one tile), and for larger trees the heads per
-// tile that need the fewest tiles at max_nodes (64 tokens x 6 heads: 2 heads x 64
-// tokens in 3 tiles, where whole tokens would take 4).
-void ta_tilings(int G, int max_nodes, TaTiling (&t)[2]) {
-  auto make = [&](int gb) { return TaTiling{gb, std::min(kTaRows / gb, max_nodes), (G + gb - 1) / gb}; };
-  t[0] = make(G);
-  t[1] = t[0];
-  auto tiles = [&](const TaTiling& x) { return x.ng * ((max_nodes + x.nb - 1) / x.nb); };
-  for (int gb = G - 1; gb >= 1; --gb)
-    if (tiles(make(gb)) < tiles(t[1])) t[1] = make(gb);
-}
-
 struct TaLayout {
   size_t seqs, items, pml, po, total;
 };
 
-TaLayout ta_layout(const TaTiling (&t)[2], int dim, int Hkv, int G, int n_batch, int max_nodes, int grid) {
-  const long long nm = std::max(1, t[1].ng * ((max_nodes + t[1].nb - 1) / t[1].nb));
+TaLayout ta_layout(int dim, int Hkv, int G, int n_batch, int max_nodes, int grid) {
+  const long long nm = (max_nodes * G + kTaRows - 1) / kTaRows;
   const long long items = (long long)n_batch * Hkv * nm + (long long)grid * kTaWaves;
   const long long rows = (long long)grid * kTaSplitItems * std::min(kTaRows, max_nodes * G);
   TaLayout l;
@@ -972,10 +951,7 @@ size_t qhl_tree_attention_workspace(const qhl_kv_pages* kv, int n_q_heads, int n
     verify_cuda_err(me, e);
     return 0;
   }
-  const int G = n_q_heads / kv->kv_heads;
-  TaTiling t[2];
-  ta_tilings(G, max_nodes, t);
-  return ta_layout(t, kv->dim, kv->kv_heads, G, n_batch, max_nodes, sms).total;
+  return ta_layout(kv->dim, kv->kv_heads, n_q_heads / kv->kv_heads, n_batch, max_nodes, sms).total;
 }
 
 int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_rows, int n_batch, int max_nodes,
@@ -1004,8 +980,7 @@ int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_r
   if (e != cudaSuccess) return verify_cuda_err(me, e);
   const int dim = kv->dim, G = n_q_heads / kv->kv_heads, KT = dim == 256 ? 64 : 128, CH = dim / 64, P = kv->page_rows;
   const bool bf16 = kv->dtype == QHL_BF16;
-  ta_tilings(G, max_nodes, a.tiling);
-  const TaLayout l = ta_layout(a.tiling, dim, kv->kv_heads, G, n_batch, max_nodes, a.grid);
+  const TaLayout l = ta_layout(dim, kv->kv_heads, G, n_batch, max_nodes, a.grid);
   if (workspace_bytes < l.total)
     return verify_err(me, STAGE_E_ARG, "the workspace needs " + std::to_string(l.total) + " bytes");
   a.box = std::min(P, KT);
@@ -1016,15 +991,12 @@ int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_r
   const int pb[4] = {a.box, a.box == KT ? CH : 1, 1, 1};
   const long long nd[4] = {n_rows, CH, kv->kv_heads, 1}, ns[4] = {new_stride, 64, dim, 64};
   const int nb[4] = {a.dbox, a.dbox == KT ? CH : 1, 1, 1};
-  const long long qd[4] = {G, n_rows, CH, kv->kv_heads}, qs[4] = {dim, q_stride, 64, (long long)G * dim};
-  bool fine = encode(&a.k, bf16, kb, pd, ps, pb) && encode(&a.v, bf16, vb, pd, ps, pb) && encode(&a.kn, bf16, k_new_dev, nd, ns, nb) &&
+  const bool fine = encode(&a.k, bf16, kb, pd, ps, pb) && encode(&a.v, bf16, vb, pd, ps, pb) && encode(&a.kn, bf16, k_new_dev, nd, ns, nb) &&
               encode(&a.vn, bf16, v_new_dev, nd, ns, nb);
-  for (int i = 0; i < 2; ++i) {
-    const int qb[4] = {a.tiling[i].gb, a.tiling[i].nb, 1, 1};
-    fine = fine && encode(&a.q[i], bf16, q_dev, qd, qs, qb);
-  }
   if (!fine) return verify_err(me, STAGE_E_UNSUPPORTED, "the driver refused a tensor map for these strides");
-  a.page_rows = P;
+  auto log2i = [](int x) { int n = 0; while (1 << n < x) ++n; return n; };
+  a.box_shift = log2i(a.box);
+  a.page_shift = log2i(P);
   a.n_pages = kv->n_pages;
   a.max_pages = kv->max_pages;
   a.n_seqs = kv->n_seqs;
@@ -1038,6 +1010,8 @@ int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_r
   a.seq = seq_dev;
   a.q_start = q_start_dev;
   a.parent = parent_dev;
+  a.q = q_dev;
+  a.q_stride = q_stride;
   a.v_new = v_new_dev;
   a.new_stride = new_stride;
   a.out = out_dev;
