@@ -408,68 +408,37 @@ def qhl_debug_inject(fault_item: int = -1, wait_limit: int = 0):
 
 # ---------------------------------------------------------------------------
 # verification of trees of drafted tokens over a paged KV cache
+#
+# These calls are short and many, so their arguments are checked and passed on
+# natively (csrc/marshal.cpp): a wrong tensor raises ValueError, a refusal of the
+# C call StageError.  They run on the device of their tensors, on its current
+# stream unless `stream` is given.
 
 QHL_F32, QHL_F16, QHL_BF16 = 0, 1, 2
 MAX_NODES = 128
-_DTYPES = {"torch.float32": QHL_F32, "torch.float16": QHL_F16, "torch.bfloat16": QHL_BF16}
+
+_native = None
 
 
-def _dtype_id(t) -> int:
-    return _DTYPES.get(str(t.dtype), -1)
+def _bound():
+    """The native marshalling module, bound to the loaded library."""
+    global _native
+    if _native is None:
+        L = lib()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise ImportError(f"the native marshalling module is missing ({e}): build it with "
+                              "`python quantized_hybrid_layer_b200/build.py`") from e
+        m.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+            "qhl_qk_norm_rope", "qhl_tree_attention", "qhl_tree_attention_workspace", "qhl_deltanet_tree", "qhl_pages_free",
+            "qhl_pages_fork", "qhl_pages_extend", "qhl_pages_commit")))
+        _native = m
+    return _native
 
 
-def _want(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
-def _ints(t, name: str, device, shape=None):
-    """A contiguous int32 tensor on `device` (of `shape`): its address."""
-    if str(t.dtype) != "torch.int32" or t.device != device or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be a contiguous int32 tensor{'' if shape is None else f' {list(shape)}'} on {device}, got "
-                         f"{t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _heads(t, name: str, device, dtype: int, heads: int, dim: int, rows: int | None = None):
-    """A [rows, heads, dim] tensor of 16-bit elements whose rows may be strided (heads and elements are
-    not): its row stride."""
-    if not (t.dim() == 3 and t.device == device and _dtype_id(t) == dtype and t.shape[1] == heads and t.shape[2] == dim
-            and (rows is None or t.shape[0] == rows) and (t.shape[0] == 0 or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == dim)))):
-        raise ValueError(f"{name} must be a [{'rows' if rows is None else rows}, {heads}, {dim}] tensor of type {dtype} with contiguous "
-                         f"heads on {device}, got {t.dtype} {list(t.shape)} strides {t.stride()} on {t.device}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
-
-
-class _On:
-    """The device of a call's tensors made current, and the stream it runs on (the device's current one unless given)."""
-
-    def __init__(self, device, stream):
-        import torch
-        _want(device.type == "cuda", f"the tensors must be on a CUDA device, got {device}")
-        self._device = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
-        self._given, self._index = stream, device.index
-
-    def __enter__(self):
-        import torch
-        if self._device is not None:
-            self._device.__enter__()
-        if self._given is None:
-            return torch.cuda.current_stream(self._index).cuda_stream
-        return getattr(self._given, "cuda_stream", self._given)
-
-    def __exit__(self, *exc):
-        if self._device is not None:
-            self._device.__exit__(*exc)
-
-    def scratch(self, nbytes: int, stream: int):
-        """Device memory for one call, which the allocator gives out again only behind `stream`."""
-        import torch
-        if self._given is None:
-            return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{self._index}")
-        s = self._given if hasattr(self._given, "cuda_stream") else torch.cuda.ExternalStream(stream, device=f"cuda:{self._index}")
-        with torch.cuda.stream(s):
-            return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{self._index}")
+def _stream_of(stream):
+    return None if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 class KvPages:
@@ -484,65 +453,46 @@ class KvPages:
     """
 
     def __init__(self, k, v, table, lens, held, refs):
-        _want(k.dim() == 5 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype and k.device == v.device
-              and k.stride(4) == 1, f"k and v must be alike, [layers, pages, kv_heads, page_rows, dim] with contiguous elements, got "
-              f"{list(k.shape)} strides {k.stride()} and {list(v.shape)} strides {v.stride()}")
-        _want(_dtype_id(k) in (QHL_F16, QHL_BF16), f"k and v must be float16 or bfloat16, got {k.dtype}")
+        dtype = {"torch.float16": QHL_F16, "torch.bfloat16": QHL_BF16}.get(str(k.dtype))
+        if not (k.dim() == 5 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype and k.device == v.device
+                and k.stride(4) == 1 and dtype is not None):
+            raise ValueError("k and v must be alike, float16 or bfloat16 [layers, pages, kv_heads, page_rows, dim] with contiguous "
+                             f"elements, got {k.dtype} {list(k.shape)} strides {k.stride()} on {k.device} and {v.dtype} {list(v.shape)} "
+                             f"strides {v.stride()} on {v.device}")
         L, N, H, P, D = k.shape
-        _want(table.dim() == 2, f"table must be [sequences, max_pages], got {list(table.shape)}")
+        if table.dim() != 2:
+            raise ValueError(f"table must be [sequences, max_pages], got {list(table.shape)}")
         S, M = table.shape
-        self.device, self.dtype = k.device, _dtype_id(k)
+        for t, name, shape in ((table, "table", (S, M)), (lens, "lens", (S,)), (held, "held", (S,)), (refs, "refs", (N,))):
+            if str(t.dtype) != "torch.int32" or t.device != k.device or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {k.device}, got {t.dtype} {list(t.shape)} on {t.device}")
         self.k, self.v, self.table, self.lens, self.held, self.refs = k, v, table, lens, held, refs
         self.layers, self.pages, self.kv_heads, self.page_rows, self.dim, self.seqs, self.max_pages = L, N, H, P, D, S, M
-        # a stride along an axis of one element is never used: any that the checks accept will do
+        # the stride along an axis of one element is never used: any that the checks accept will do
         st = [k.stride(a) if k.shape[a] > 1 else max(D, 8) for a in range(4)]
-        self._c = KvPagesStruct(k.data_ptr(), v.data_ptr(), self.dtype, L, N, H, P, D, st[0], st[1], st[2], st[3], S, M,
-                                _ints(table, "table", k.device), _ints(lens, "lens", k.device, (S,)),
-                                _ints(held, "held", k.device, (S,)), _ints(refs, "refs", k.device, (N,)))
-        self._p = ctypes.byref(self._c)
-        self._workspace = {}
+        self._c = KvPagesStruct(k.data_ptr(), v.data_ptr(), dtype, L, N, H, P, D, st[0], st[1], st[2], st[3], S, M, table.data_ptr(),
+                                lens.data_ptr(), held.data_ptr(), refs.data_ptr())
+        self._at, self._dev = ctypes.addressof(self._c), k.get_device()
 
 
 def qhl_qk_norm_rope(n_q_heads: int, n_kv_heads: int, dim: int, rope_dims: int, theta: float, eps: float, y, pos, gamma_q, gamma_k,
-                     q, k, v, offsets=None, stream=None):
+                     q, k, v, offsets=(-1, -1, -1), stream=None):
     """Norm of every query and key head and rotation by position, from in-projection rows y [n, width] (f32, f16 or
-    bf16; rows may be strided) to q [n, n_q_heads, dim] and k, v [n, n_kv_heads, dim] (f16 or bf16).  offsets: where q, k
-    and v begin in a row; by default the order q | gate | k | v of a stage's in-projection."""
-    dev, n = y.device, y.shape[0]
-    _want(y.dim() == 2 and _dtype_id(y) >= 0 and (n == 0 or y.stride(1) == 1), "y must be [rows, width] of f32, f16 or bf16 with contiguous rows")
-    qw, kw = n_q_heads * dim, n_kv_heads * dim
-    off = (0, 2 * qw, 2 * qw + kw) if offsets is None else offsets
-    _want(min(off) >= 0 and off[0] + qw <= y.shape[1] and max(off[1], off[2]) + kw <= y.shape[1],
-          f"y rows of {y.shape[1]} elements do not hold {n_q_heads} query and {n_kv_heads} key and value heads at {tuple(off)}")
-    for t, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
-        _want(t.device == dev and str(t.dtype) == "torch.float32" and tuple(t.shape) == (dim,) and t.is_contiguous(),
-              f"{name} must be a contiguous float32 tensor [{dim}] on {dev}")
-    dt = _dtype_id(q)
-    _want(dt in (QHL_F16, QHL_BF16), "q, k and v must be float16 or bfloat16")
-    qs, ks, vs = _heads(q, "q", dev, dt, n_q_heads, dim, n), _heads(k, "k", dev, dt, n_kv_heads, dim, n), _heads(v, "v", dev, dt, n_kv_heads, dim, n)
-    pp = _ints(pos, "pos", dev, (n,))
-    if n == 0:
-        return q, k, v
-    on = _On(dev, stream)
-    with on as s:
-        _check_qhl(lib().qhl_qk_norm_rope(n_q_heads, n_kv_heads, dim, rope_dims, theta, eps, y.data_ptr(), _dtype_id(y),
-                                          y.stride(0) if n > 1 else max(y.stride(0), y.shape[1]), off[0], off[1], off[2], n, pp,
-                                          gamma_q.data_ptr(), gamma_k.data_ptr(), dt, q.data_ptr(), qs, k.data_ptr(), ks,
-                                          v.data_ptr(), vs, s))
+    bf16; rows may be strided) to q [n, n_q_heads, dim] and k, v [n, n_kv_heads, dim] (f16 or bf16; rows may be
+    strided).  pos int32 [n]; gamma_q, gamma_k f32 [dim].  offsets: where q, k and v begin in a row; by default the
+    order q | gate | k | v of a stage's in-projection."""
+    rc = (_native or _bound()).norm_rope(n_q_heads, n_kv_heads, dim, rope_dims, theta, eps, y, pos, gamma_q, gamma_k, q, k, v, *offsets,
+                                           _stream_of(stream))
+    if rc:
+        _check_qhl(rc)
     return q, k, v
 
 
 def qhl_tree_attention_workspace(kv: KvPages, n_q_heads: int, n_rows: int, n_batch: int, max_nodes: int) -> int:
     """Bytes of workspace that qhl_tree_attention needs; raises where it would refuse these sizes."""
-    key = (n_q_heads, n_rows, n_batch, max_nodes)
-    n = kv._workspace.get(key)
-    if n is None:
-        n = int(lib().qhl_tree_attention_workspace(kv._p, *key))
-        if n == 0:
-            raise StageError(-1, lib().qhl_last_error().decode())
-        if len(kv._workspace) >= 256:
-            kv._workspace.clear()
-        kv._workspace[key] = n
+    n = int(lib().qhl_tree_attention_workspace(ctypes.byref(kv._c), n_q_heads, n_rows, n_batch, max_nodes))
+    if n == 0:
+        raise StageError(-1, lib().qhl_last_error().decode())
     return n
 
 
@@ -551,30 +501,11 @@ def qhl_tree_attention(kv: KvPages, layer: int, seqs, q_start, parent, max_nodes
     """Attention of the trees of drafted tokens q_start, parent (int32; see qhl_stage.h) over layer `layer` of a paged
     cache and over their own keys and values: q, out [n_rows, n_q_heads, dim], k_new, v_new [n_rows, kv_heads, dim] in
     the cache's type (rows may be strided); lse f32 [n_rows, n_q_heads] if given.  scale: 1 / sqrt(dim) by default.
-    workspace: a uint8 tensor of at least qhl_tree_attention_workspace bytes; by default the caching allocator's."""
-    dev = kv.device
-    _want(q.dim() == 3, "q must be [n_rows, n_q_heads, dim]")
-    n, hq, b, H, D = q.shape[0], q.shape[1], seqs.shape[0], kv.kv_heads, kv.dim
-    qs, os_ = _heads(q, "q", dev, kv.dtype, hq, D), _heads(out, "out", dev, kv.dtype, hq, D, n)
-    ns = _heads(k_new, "k_new", dev, kv.dtype, H, D, n)
-    _want(_heads(v_new, "v_new", dev, kv.dtype, H, D, n) == ns, "k_new and v_new must have the same strides")
-    if lse is not None:
-        _want(lse.device == dev and str(lse.dtype) == "torch.float32" and tuple(lse.shape) == (n, hq) and lse.is_contiguous(),
-              f"lse must be a contiguous float32 tensor [{n}, {hq}] on {dev}")
-    sp, qp, pp = _ints(seqs, "seqs", dev, (b,)), _ints(q_start, "q_start", dev, (b + 1,)), _ints(parent, "parent", dev, (n,))
-    if n == 0:
-        return out
-    on = _On(dev, stream)
-    with on as s:
-        need = qhl_tree_attention_workspace(kv, hq, n, b, max_nodes)
-        if workspace is None:
-            workspace = on.scratch(need, s)
-        else:
-            _want(workspace.device == dev and workspace.is_contiguous(), f"workspace must be a contiguous tensor on {dev}")
-        _check_qhl(lib().qhl_tree_attention(kv._p, layer, hq, n, b, max_nodes, sp, qp, pp, q.data_ptr(), qs, k_new.data_ptr(),
-                                            v_new.data_ptr(), ns, out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
-                                            D ** -0.5 if scale is None else scale, workspace.data_ptr(),
-                                            workspace.numel() * workspace.element_size(), s))
+    workspace: a tensor of at least qhl_tree_attention_workspace bytes; by default the caching allocator's."""
+    rc = (_native or _bound()).tree_attention(kv._at, kv._dev, layer, seqs, q_start, parent, max_nodes, q, k_new, v_new, out, lse, scale,
+                                                workspace, _stream_of(stream))
+    if rc:
+        _check_qhl(rc)
     return out
 
 
@@ -582,70 +513,41 @@ def qhl_deltanet_tree(Hk: int, Hv: int, y, q_start, parent, max_nodes: int, stat
     """The gated DeltaNet step along trees of drafted tokens (qhl_deltanet_step with a parent per token): y f32
     [n_rows, 2 Hk 128 + Hv 128 + 2 Hv], states f32 [n_states, Hv, 128, 128], state_index int32 [batch] (-1: zero),
     snaps f32 [n_rows, Hv, 128, 128] and o f32 [n_rows, Hv * 128] receive each token's state and output."""
-    dev, n, b = y.device, y.shape[0], state_index.shape[0]
-    for t, name, shape in ((y, "y", (n, 2 * Hk * 128 + Hv * 128 + 2 * Hv)), (states, "states", (states.shape[0], Hv, 128, 128)),
-                           (snaps, "snaps", (n, Hv, 128, 128)), (o, "o", (n, Hv * 128))):
-        if t.device != dev or str(t.dtype) != "torch.float32" or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape)} on {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
-    ip, qp, pp = _ints(state_index, "state_index", dev, (b,)), _ints(q_start, "q_start", dev, (b + 1,)), _ints(parent, "parent", dev, (n,))
-    if n == 0:
-        return o
-    on = _On(dev, stream)
-    with on as s:
-        _check_qhl(lib().qhl_deltanet_tree(Hk, Hv, y.data_ptr(), n, b, max_nodes, qp, pp, states.data_ptr(), states.shape[0], ip,
-                                           snaps.data_ptr(), o.data_ptr(), s))
+    rc = (_native or _bound()).deltanet_tree(Hk, Hv, y, q_start, parent, max_nodes, states, state_index, snaps, o, _stream_of(stream))
+    if rc:
+        _check_qhl(rc)
     return o
 
 
 def qhl_pages_free(kv: KvPages, seqs, status, stream=None):
     """Sequences let go of their pages.  status: int32 [n], a stage_status for each request (as in the calls below)."""
-    n = seqs.shape[0]
-    with _On(kv.device, stream) as s:
-        _check_qhl(lib().qhl_pages_free(kv._p, n, _ints(seqs, "seqs", kv.device, (n,)), _ints(status, "status", kv.device, (n,)), s))
+    rc = (_native or _bound()).pages_free(kv._at, kv._dev, seqs, status, _stream_of(stream))
+    if rc:
+        _check_qhl(rc)
     return status
 
 
 def qhl_pages_fork(kv: KvPages, src, dst, status, stream=None):
     """Each dst becomes a copy of its src that shares the pages of its committed rows."""
-    n = src.shape[0]
-    with _On(kv.device, stream) as s:
-        _check_qhl(lib().qhl_pages_fork(kv._p, n, _ints(src, "src", kv.device, (n,)), _ints(dst, "dst", kv.device, (n,)),
-                                        _ints(status, "status", kv.device, (n,)), s))
+    rc = (_native or _bound()).pages_fork(kv._at, kv._dev, src, dst, status, _stream_of(stream))
+    if rc:
+        _check_qhl(rc)
     return status
 
 
 def qhl_pages_extend(kv: KvPages, seqs, add, status, workspace=None, stream=None):
-    """Room for add more rows in pages that each sequence alone holds.  workspace: 16 bytes per request."""
-    n = seqs.shape[0]
-    on = _On(kv.device, stream)
-    with on as s:
-        if workspace is None:
-            workspace = on.scratch(16 * max(n, 1), s)
-        else:
-            _want(workspace.device == kv.device and workspace.is_contiguous(), f"workspace must be a contiguous tensor on {kv.device}")
-        _check_qhl(lib().qhl_pages_extend(kv._p, n, _ints(seqs, "seqs", kv.device, (n,)), _ints(add, "add", kv.device, (n,)),
-                                          _ints(status, "status", kv.device, (n,)), workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), s))
+    """Room for add more rows in pages that each sequence alone holds.  workspace: 16 bytes per request; by default the
+    caching allocator's."""
+    rc = (_native or _bound()).pages_extend(kv._at, kv._dev, seqs, add, status, workspace, _stream_of(stream))
+    if rc:
+        _check_qhl(rc)
     return status
 
 
 def qhl_pages_commit(kv: KvPages, seqs, q_start, path, n_accepted, pos, k_new, v_new, status, stream=None):
     """The accepted path of each tree into its sequence's pages from row pos on, in every layer: path int32 [batch, most],
     its first n_accepted entries are tokens of the tree; k_new, v_new [layers, n_rows, kv_heads, dim]."""
-    b, dev = seqs.shape[0], kv.device
-    _want(path.dim() == 2, "path must be [batch, most]")
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _want(t.dim() == 4 and t.device == dev and _dtype_id(t) == kv.dtype and t.shape[0] == kv.layers and t.shape[2] == kv.kv_heads
-              and t.shape[3] == kv.dim and t.stride(3) == 1 and (kv.kv_heads == 1 or t.stride(2) == kv.dim),
-              f"{name} must be [{kv.layers}, rows, {kv.kv_heads}, {kv.dim}] in the cache's type with contiguous heads on {dev}, got "
-              f"{t.dtype} {list(t.shape)} strides {t.stride()} on {t.device}")
-    _want(k_new.shape == v_new.shape and k_new.stride() == v_new.stride(), "k_new and v_new must be alike")
-    rows = k_new.shape[1]
-    sr = k_new.stride(1) if rows > 1 else kv.kv_heads * kv.dim
-    sl = k_new.stride(0) if kv.layers > 1 else sr
-    with _On(dev, stream) as s:
-        _check_qhl(lib().qhl_pages_commit(kv._p, b, rows, _ints(seqs, "seqs", dev, (b,)), _ints(q_start, "q_start", dev, (b + 1,)),
-                                          _ints(path, "path", dev, (b, path.shape[1])), path.shape[1],
-                                          _ints(n_accepted, "n_accepted", dev, (b,)), _ints(pos, "pos", dev, (b,)), k_new.data_ptr(),
-                                          v_new.data_ptr(), sl, sr, _ints(status, "status", dev, (b,)), s))
+    rc = (_native or _bound()).pages_commit(kv._at, kv._dev, seqs, q_start, path, n_accepted, pos, k_new, v_new, status, _stream_of(stream))
+    if rc:
+        _check_qhl(rc)
     return status

@@ -3,7 +3,9 @@
 Every source under csrc/ is compiled with
 ``-gencode arch=compute_100a,code=sm_100a -O3 -lineinfo`` (no fast-math) and
 linked into one shared object beside this file, with the CUDA runtime linked
-statically so the library is self-contained.
+statically so the library is self-contained.  The native marshalling of the
+tree-verification calls (csrc/marshal.cpp, host code against PyTorch's headers)
+becomes an extension module of its own, so the library stays free of PyTorch.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqhl_stage.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 SOURCES = ["gemv.cu", "pass.cu", "mixers.cu", "stage.cu", "kernel_abi.cu", "noalloc.cu",
            "norm_rope.cu", "tree_attention.cu", "deltanet_tree.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -49,12 +52,30 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_marshal():
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG", *[f"-I{p}" for p in include], os.path.join(CSRC, "marshal.cpp"),
+           "-o", tmp, f"-L{root}/lib", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{root}/lib"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime() for p in (LIB, MARSHAL)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        marshal.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:

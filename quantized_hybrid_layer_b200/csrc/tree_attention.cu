@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
                 if (!(bits >> e & 1)) sv[j][e] = 0xff800000u;
             }
           } else {
-            const int lim = alive ? w.s.ctx - tile * KT - hf * HK : 0;
+            const int lim = alive || !valid ? w.s.ctx - tile * KT - hf * HK : 0;
             if (lim < HK) {
 #pragma unroll
               for (int j = 0; j < HK / 32; ++j)

@@ -21,6 +21,50 @@ def q():
     return q
 
 
+def test_the_binding_refuses_wrong_tensors_on_the_gpu(q):
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")   # noqa: E731
+    k = torch.zeros(2, 4, 2, 16, 64, dtype=torch.float16, device="cuda")
+    kv = q.KvPages(k, k.clone(), i32(3, 2), i32(3), i32(3), i32(4))
+    x, n = torch.zeros(2, 4, 64, dtype=torch.float16, device="cuda"), torch.zeros(2, 2, 64, dtype=torch.float16, device="cuda")
+
+    def refused(f, good, bad):
+        f(**good)
+        for o in bad:
+            with pytest.raises((ValueError, q.StageError)):
+                f(**{**good, **o})
+
+    refused(q.qhl_tree_attention, dict(kv=kv, layer=0, seqs=i32(1), q_start=i32(2), parent=i32(2) - 1, max_nodes=2, q=x, k_new=n, v_new=n, out=x.clone()),
+            [dict(q=x.bfloat16()), dict(q=x.transpose(0, 1)), dict(q=x.cpu()), dict(k_new=x), dict(v_new=torch.cat([n, n], 1)[:, :2]), dict(out=x[:1]),
+             dict(lse=torch.zeros(2, 2, device="cuda")), dict(lse=torch.zeros(2, 4)), dict(parent=i32(3)), dict(parent=i32(2).long()), dict(q_start=i32(1)),
+             dict(seqs=i32(1).cpu()), dict(seqs=i32(1, 1)), dict(layer=2), dict(max_nodes=0), dict(max_nodes=129), dict(scale=-1.0), dict(scale="x"),
+             dict(workspace=torch.zeros(64, dtype=torch.uint8, device="cuda")), dict(workspace=torch.zeros(1 << 24, dtype=torch.uint8)), dict(stream="x")])
+    y, p = torch.zeros(2, 768, device="cuda"), i32(2)
+    one = torch.ones(64, device="cuda")
+    refused(lambda **a: q.qhl_qk_norm_rope(4, 2, 64, a.get("rope", 64), 1e4, 1e-6, *(a[c] for c in ("y", "p", "gq", "gk", "q", "k", "v")), **a["kw"]),
+            dict(y=y, p=p, gq=one, gk=one, q=x, k=n, v=n.clone(), kw={}),
+            [dict(y=y[:, :760]), dict(y=y.double()), dict(y=y.cpu()), dict(y=y.t()), dict(p=p[:1]), dict(p=p.long()), dict(gq=one[:32]), dict(gk=one.half()),
+             dict(q=x.float()), dict(k=n.bfloat16()), dict(v=n[:1]), dict(rope=60), dict(kw=dict(offsets=(0, 640, 700))), dict(kw=dict(offsets=(0, -8, 640)))])
+    st, sn = torch.zeros(1, 4, 128, 128, device="cuda"), torch.zeros(2, 4, 128, 128, device="cuda")
+    refused(lambda **a: q.qhl_deltanet_tree(4, 4, a["y"], a["s"], a["p"], 2, a["st"], a["ix"], a["sn"], a["o"]),
+            dict(y=torch.zeros(2, 1544, device="cuda"), s=i32(2), p=i32(2) - 1, st=st, ix=i32(1), sn=sn, o=torch.zeros(2, 512, device="cuda")),
+            [dict(y=torch.zeros(2, 1540, device="cuda")), dict(s=i32(1)), dict(p=i32(3)), dict(st=st[:, :2]), dict(st=st.half()), dict(sn=sn[:1]),
+             dict(st=sn), dict(o=torch.zeros(2, 512)), dict(ix=i32(1).long())])
+    for f, good in ((q.qhl_pages_free, (i32(1), i32(1))), (q.qhl_pages_fork, (i32(1), i32(1) + 1, i32(1))), (q.qhl_pages_extend, (i32(1), i32(1), i32(1)))):
+        f(kv, *good)
+        for at in range(len(good)):
+            for bad in (good[at].long(), i32(2), good[at].cpu()):
+                with pytest.raises(ValueError):
+                    f(kv, *good[:at], bad, *good[at + 1:])
+        with pytest.raises(q.StageError):
+            f(kv, *(g[:0] for g in good))                # no requests
+    new = torch.zeros(2, 2, 2, 64, dtype=torch.float16, device="cuda")
+    refused(lambda **a: q.qhl_pages_commit(kv, a["s"], a["q"], a["p"], a["n"], a["at"], a["k"], a["v"], a["st"]),
+            dict(s=i32(1), q=i32(2), p=i32(1, 2), n=i32(1), at=i32(1), k=new, v=new, st=i32(1)),
+            [dict(s=i32(2)), dict(q=i32(1)), dict(p=i32(2)), dict(p=i32(2, 2)), dict(n=i32(2)), dict(at=i32(1).cpu()), dict(k=new[:1]), dict(v=new.float()),
+             dict(k=new.transpose(1, 2)), dict(st=i32(0))])
+    q.qhl_sync()
+
+
 # ------------------------------------------------------------- norm and rope
 
 def check_norm_rope(q, n, hq, hkv, dim, rope, src, dst, theta=1e7, far=262144, seed=0, pad=0, offsets=None):
