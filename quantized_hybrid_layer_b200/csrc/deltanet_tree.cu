@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(256) dn_tree_kernel(const DnTreeArgs a) {
   const size_t state_elems = (size_t)a.Hv * kDnDim * kDnDim;
   const size_t mine = ((size_t)h * kDnDim + row0) * kDnDim + 4 * lane;   // this lane's element of row 0 of its warp
 
+  if (tid == 0) pdl_launch();
+  pdl_wait();
   int first, n;
   tree_rows(a.q_start, blockIdx.y, a.n_rows, a.max_nodes, first, n, a.err);
   if (n == 0) return;
@@ -207,7 +209,6 @@ extern "C" int qhl_deltanet_tree(int Hk, int Hv, const float* y_dev, int n_rows,
                   state_index_dev, snaps_dev, o_dev, nullptr};
   cudaError_t e = verify_error_word(&a.err);
   if (e != cudaSuccess) return verify_cuda_err(me, e);
-  dn_tree_kernel<<<dim3(Hv * 4, n_batch), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  e = cudaGetLastError();
+  e = launch_ex(dn_tree_kernel, dim3(Hv * 4, n_batch), dim3(256), 0, static_cast<cudaStream_t>(stream), true, a);
   return e == cudaSuccess ? 0 : verify_cuda_err(me, e);
 }

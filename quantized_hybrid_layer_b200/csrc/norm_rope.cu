@@ -79,7 +79,9 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nvec = a.hq + 2 * a.hkv, per_row = (nvec + V - 1) / V;
   const long long task = (long long)blockIdx.x * 8 + warp;
+  if (threadIdx.x == 0) pdl_launch();
   if (task >= (long long)a.n_rows * per_row) return;
+  pdl_wait();
   const int row = (int)(task / per_row), v0 = (int)(task % per_row) * V;
   const bool on = D >= 128 || 4 * lane < D;
 
@@ -176,11 +178,8 @@ static cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
   const bool many = (long long)a.n_rows * nvec >= 148LL * 64 * 4;
   const long long tasks = (long long)a.n_rows * (many ? (nvec + 3) / 4 : nvec);
   const unsigned grid = (unsigned)((tasks + 7) / 8);
-  if (many)
-    norm_rope_kernel<SRC, DST, D, 4><<<grid, 256, 0, s>>>(a);
-  else
-    norm_rope_kernel<SRC, DST, D, 1><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return many ? launch_ex(norm_rope_kernel<SRC, DST, D, 4>, dim3(grid), dim3(256), 0, s, true, a)
+              : launch_ex(norm_rope_kernel<SRC, DST, D, 1>, dim3(grid), dim3(256), 0, s, true, a);
 }
 
 template <typename SRC, typename DST>

@@ -13,6 +13,9 @@
 // over refs, 4 bytes per page), a second grid copies the shared last pages'
 // committed rows; bound by those rows, read and written once.  commit: one CTA
 // per (tree, layer, K or V), 16-byte moves, bound by the accepted rows.
+// Every kernel is launched as a programmatic dependent of the one before it on
+// the stream and waits for that one's end before it reads anything, which hides
+// most of a launch (about 1 us of a chain of short calls).
 #include <mutex>
 
 #include "launch.h"
@@ -134,6 +137,8 @@ QHL_DEV bool named_before(const int* seq, int i, int s) {
 // -------------------------------------------------------------------- free --
 
 __global__ void __launch_bounds__(128) pages_free_kernel(const PagesView p, const int* seq, int* status) {
+  if (threadIdx.x == 0) pdl_launch();
+  pdl_wait();
   const int i = blockIdx.x, s = __ldg(seq + i);
   const bool dup = named_before(seq, i, s);
   if (s < 0 || s >= p.n_seqs || dup) {
@@ -161,6 +166,8 @@ __global__ void __launch_bounds__(128) pages_free_kernel(const PagesView p, cons
 // -------------------------------------------------------------------- fork --
 
 __global__ void __launch_bounds__(128) pages_fork_kernel(const PagesView p, int n, const int* src, const int* dst, int* status) {
+  if (threadIdx.x == 0) pdl_launch();
+  pdl_wait();
   const int i = blockIdx.x, s = __ldg(src + i), d = __ldg(dst + i);
   bool again = false;   // dst named before, or src a dst of this call
   for (int j = threadIdx.x; j < n; j += 128) {
@@ -231,10 +238,12 @@ QHL_DEV int block_scan(int v, int* warp_sums, int& total) {
 // free page of rank f goes to the request whose range of the prefix sum holds f.
 __global__ void __launch_bounds__(1024) pages_extend_kernel(const PagesView p, int n, const int* seq, const int* add, int* status,
                                                             PageCopy* copies) {
-  __shared__ int s_seq[kMaxRequests], s_last[kMaxRequests], s_end[kMaxRequests], s_at[kMaxRequests], s_copied[kMaxRequests];
+  __shared__ int s_seq[kMaxRequests], s_last[kMaxRequests], s_end[kMaxRequests], s_at[kMaxRequests], s_copied[kMaxRequests],
+      s_held[kMaxRequests];
   __shared__ int s_warp[32];
   const int tid = threadIdx.x, P = p.rows;
   if (tid == 0) pdl_launch();
+  pdl_wait();
   const int s = tid < n ? __ldg(seq + tid) : -1;
   const int more = tid < n ? __ldg(add + tid) : 0;
   s_seq[tid] = s;
@@ -290,55 +299,62 @@ __global__ void __launch_bounds__(1024) pages_extend_kernel(const PagesView p, i
   int total;
   const int begin = block_scan(need, s_warp, total);
   s_end[tid] = begin + need;
-  s_at[tid] = copied ? last_at : held;       // table index of the request's first new page
+  s_at[tid] = last_at;                       // table index of the page that is copied
   s_copied[tid] = copied;
-  // free pages in all, as far as they are needed (16 pages a thread and step)
-  int have = 0;
-  const int sweep = 1024 * 16;
-  for (long long base = 0; base < p.n_pages && have < total; base += sweep) {
-    int c = 0;
+  s_held[tid] = held;
+  // Free pages in all, as far as they are needed, and then their hand-out in
+  // ascending order.  A thread looks at 16 consecutive pages of a sweep; a pool of
+  // one sweep is read once for both.
+  constexpr int kSweep = 1024 * 16;
+  auto free_of = [&](long long base) {       // a bit for each free page of the thread's 16
+    unsigned bits = 0;
+    const long long p0 = base + tid * 16;
+    int r[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const long long pg = base + (long long)j * 1024 + tid;
-      c += pg < p.n_pages && p.refs[pg] == 0;
-    }
-    int t;
-    block_scan(c, s_warp, t);
-    have += t;
+    for (int j = 0; j < 16; ++j) r[j] = p0 + j < p.n_pages ? p.refs[p0 + j] : 1;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) bits |= (r[j] == 0 ? 1u : 0u) << j;
+    return bits;
+  };
+  int have = 0, sweep_free = 0;
+  unsigned bits = 0;
+  int rank = 0;
+  for (long long base = 0; base < p.n_pages && have < total; base += kSweep) {
+    bits = free_of(base);
+    rank = block_scan(__popc(bits), s_warp, sweep_free);
+    have += sweep_free;
   }
   __syncthreads();
   if (tid < n && rc == STAGE_OK && s_end[tid] > have && (need > 0 || refs > 1)) rc = STAGE_E_OOM;
   const bool ok = tid < n && rc == STAGE_OK;
-  // hand out pages in ascending order: threads take consecutive pages of a step
   int given = 0;
-  for (long long base = 0; base < p.n_pages && given < min(have, total); base += 1024) {
-    const long long pg = base + tid;
-    const bool is_free = pg < p.n_pages && p.refs[pg] == 0;
-    int t;
-    const int f = given + block_scan(is_free, s_warp, t);
-    if (is_free && f < total) {
-      int lo = 0, hi = n - 1;                // first request whose range ends beyond f
+  for (long long base = 0; base < p.n_pages && given < min(have, total); base += kSweep) {
+    if (p.n_pages > kSweep) {
+      bits = free_of(base);
+      rank = block_scan(__popc(bits), s_warp, sweep_free);
+    }
+    int f = given + rank;
+    for (unsigned left = bits; left && f < total; left &= left - 1, ++f) {
+      const int pg = (int)(base + tid * 16) + __ffs(left) - 1;
+      int lo = 0, hi = n - 1;                // the first request whose range ends beyond f
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
         if (s_end[mid] > f) hi = mid;
         else lo = mid + 1;
       }
-      const int lo_begin = lo ? s_end[lo - 1] : 0;
-      if (s_end[lo] <= have) {               // granted
-        const int at = f - lo_begin;
-        int* row = p.table + (size_t)s_seq[lo] * p.max_pages;
-        if (s_copied[lo] && at == 0) {
-          copies[lo] = PageCopy{s_last[lo], (int)pg, 0, 0};
-          row[s_at[lo]] = (int)pg;
-        } else if (s_copied[lo]) {
-          row[p.held[s_seq[lo]] + at - 1] = (int)pg;
-        } else {
-          row[s_at[lo] + at] = (int)pg;
-        }
-        p.refs[pg] = 1;
+      if (s_end[lo] > have) break;           // not granted, nor are those behind it
+      const int at = f - (lo ? s_end[lo - 1] : 0);
+      int* row = p.table + (size_t)s_seq[lo] * p.max_pages;
+      if (s_copied[lo] && at == 0) {
+        copies[lo] = PageCopy{s_last[lo], pg, 0, 0};
+        row[s_at[lo]] = pg;
+      } else {
+        row[s_held[lo] + at - s_copied[lo]] = pg;
       }
+      p.refs[pg] = 1;
     }
-    given += t;
+    given += sweep_free;
+    if (p.n_pages > kSweep) __syncthreads();
   }
   __syncthreads();
   if (tid < n) {
@@ -355,6 +371,7 @@ __global__ void __launch_bounds__(1024) pages_extend_kernel(const PagesView p, i
 
 // One CTA per (layer, K or V, head) and request.
 __global__ void __launch_bounds__(128) pages_copy_kernel(const PagesView p, const PageCopy* copies) {
+  if (threadIdx.x == 0) pdl_launch();
   pdl_wait();
   const PageCopy c = copies[blockIdx.y];
   const int head = blockIdx.x % p.heads, z = blockIdx.x / p.heads;
@@ -401,6 +418,8 @@ __global__ void __launch_bounds__(256) pages_commit_kernel(const PagesView p, co
   __shared__ long long s_to[kMaxNodes];   // byte offset of page and row
   __shared__ int s_arg, s_state;         // whether a thread found a bad argument, a wrong state
   const int b = blockIdx.x, tid = threadIdx.x, layer = blockIdx.y >> 1, P = p.rows;
+  if (tid == 0) pdl_launch();
+  pdl_wait();
   const int s = __ldg(a.seq + b);
   if (tid == 0) s_arg = s_state = 0;
   const bool dup = named_before(a.seq, b, s);
@@ -480,8 +499,7 @@ int qhl_pages_free(const qhl_kv_pages* kv, int n, const int* seq_dev, int* statu
   int rc = check_requests(me, kv, n, seq_dev && status_dev);
   if (!rc) rc = open_pages(me, kv, &p);
   if (rc) return rc;
-  pages_free_kernel<<<n, 128, 0, static_cast<cudaStream_t>(stream)>>>(p, seq_dev, status_dev);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_ex(pages_free_kernel, dim3(n), dim3(128), 0, static_cast<cudaStream_t>(stream), true, p, seq_dev, status_dev);
   return e == cudaSuccess ? 0 : verify_cuda_err(me, e);
 }
 
@@ -491,8 +509,8 @@ int qhl_pages_fork(const qhl_kv_pages* kv, int n, const int* src_dev, const int*
   int rc = check_requests(me, kv, n, src_dev && dst_dev && status_dev);
   if (!rc) rc = open_pages(me, kv, &p);
   if (rc) return rc;
-  pages_fork_kernel<<<n, 128, 0, static_cast<cudaStream_t>(stream)>>>(p, n, src_dev, dst_dev, status_dev);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_ex(pages_fork_kernel, dim3(n), dim3(128), 0, static_cast<cudaStream_t>(stream), true, p, n, src_dev, dst_dev, status_dev);
   return e == cudaSuccess ? 0 : verify_cuda_err(me, e);
 }
 
@@ -507,7 +525,7 @@ int qhl_pages_extend(const qhl_kv_pages* kv, int n, const int* seq_dev, const in
   if ((rc = open_pages(me, kv, &p))) return rc;
   PageCopy* copies = static_cast<PageCopy*>(workspace_dev);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_ex(pages_extend_kernel, dim3(1), dim3(1024), 0, s, false, p, n, seq_dev, add_dev, status_dev, copies);
+  cudaError_t e = launch_ex(pages_extend_kernel, dim3(1), dim3(1024), 0, s, true, p, n, seq_dev, add_dev, status_dev, copies);
   if (e == cudaSuccess)
     e = launch_ex(pages_copy_kernel, dim3(p.n_layers * 2 * p.heads, n), dim3(128), 0, s, true, p, (const PageCopy*)copies);
   return e == cudaSuccess ? 0 : verify_cuda_err(me, e);
@@ -530,8 +548,8 @@ int qhl_pages_commit(const qhl_kv_pages* kv, int n_batch, int n_rows, const int*
   CommitArgs a = {seq_dev, q_start_dev, path_dev, path_stride, n_rows, n_accepted_dev, pos_dev,
                   static_cast<const uint8_t*>(k_new_dev), static_cast<const uint8_t*>(v_new_dev), new_stride_layer * 2,
                   new_stride_row * 2, status_dev};
-  pages_commit_kernel<<<dim3(n_batch, p.n_layers * 2), 256, 0, static_cast<cudaStream_t>(stream)>>>(p, a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_ex(pages_commit_kernel, dim3(n_batch, p.n_layers * 2), dim3(256), 0, static_cast<cudaStream_t>(stream), true, p, a);
   return e == cudaSuccess ? 0 : verify_cuda_err(me, e);
 }
 

@@ -84,6 +84,17 @@ QHL_DEV void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// One lane of a converged warp.
+QHL_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p)
+      :
+      : "memory");
+  return p != 0;
+}
+
 // 2^x by the hardware's approximation (relative error below 2^-22; 0 at -inf).
 QHL_DEV float ex2(float x) {
   float y;

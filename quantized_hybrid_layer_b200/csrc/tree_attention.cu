@@ -47,8 +47,8 @@ namespace qhl {
 constexpr int kTaThreads = 384;
 constexpr uint32_t kTaWait = 1u << 22;   // tries of a wait before it is given up (seconds)
 constexpr int kTaRows = 128;          // rows of an M tile
-constexpr int kTaWaves = 8;           // planned waves beyond the fewest possible
-constexpr int kTaSplitItems = 4;      // at most this many split items per SM
+constexpr int kTaOwnPlan = 256;       // trees up to which every CTA plans for itself
+constexpr int kTaStart = 2;           // tiles' time that an item's start and end take
 
 template <int DIM>
 struct TaShape {
@@ -64,10 +64,16 @@ struct TaShape {
 // One tree as the plan sees it.
 struct TaSeq {
   int row0, n, seq, ctx;
-  int chunks;        // ranges its key tiles are split into
-  int slot0;         // its first partial row
-  int tiles;
-  int pad;
+  int tiles;         // key tiles, of the cache and of the drafts
+  int nm;            // M tiles per KV head
+  long long base;    // its first unit of work
+};
+
+// The whole plan, for the join and for large batches.
+struct TaHead {
+  long long units;
+  int runs;          // none of them empty
+  short heads, tiles;   // KV heads and M tiles of a group of CTAs
 };
 
 struct TaArgs {
@@ -90,152 +96,143 @@ struct TaArgs {
   long long out_stride;
   float* lse;
   float c;                     // scale / ln 2
-  int* hdr;                    // [0]: items
+  TaHead* head;
   TaSeq* seqs;
-  int4* items;                 // tree, first tile, last tile + 1, head | m tile << 8 | range << 16
   float2* pml;                 // per partial row: c m, l
   float* po;                   // per partial row: O
+  int slot_rows;               // partial rows of a slot: an M tile's, or all there can be
   int grid;
   unsigned* err;
 };
 
 // ------------------------------------------------------------------ planning --
+//
+// The CTAs take equal runs of the work, so that all end together whatever the
+// lengths.  Work is counted in key tiles, with kTaStart more for an item's start
+// and end.  A group of CTAs shares a run: CTA j of it takes KV head and M tile j of
+// the same keys, so that rows that lie together in memory (the heads of a page,
+// the tiles that several M tiles need) are read at the same time, which HBM and L2
+// reward (4 heads, 4 x 65536 rows: 166 us with a run per CTA, 160 us in groups).
+// A segment is the key tiles of a tree for one group of heads; segments stand one
+// after the other.
+//   heads: the KV heads of a group, the most that divide the heads and leave at
+//     most 5% of the CTAs without a group.
+//   M tiles: as many as the largest tree has, unless that wastes more than 15% of
+//     the CTAs' time (trees of very different sizes); then an M tile is a segment.
+// A segment that spans several runs is joined afterwards.  A CTA has at most two
+// partial items: one that goes on from the run before (slot 0) and one that the
+// next run goes on with (slot 1).
 
+QHL_DEV int ta_segments(const TaSeq& s, const TaHead& h, int Hkv) { return Hkv / h.heads * (h.tiles > 1 ? 1 : s.nm); }
+QHL_DEV int ta_units(const TaSeq& s) { return s.tiles ? s.tiles + kTaStart : 0; }
+// First unit of run r, and the run that has unit u.
+QHL_DEV long long ta_run_start(long long units, int runs, int r) { return units * r / runs; }
+QHL_DEV int ta_run_of(long long units, int runs, long long u) { return (int)(((u + 1) * runs - 1) / units); }
+
+// Tree b, its lengths checked.
+template <int KT>
+QHL_DEV TaSeq ta_seq(const TaArgs& a, int b) {
+  TaSeq s;
+  s.seq = __ldg(a.seq + b);
+  tree_rows(a.q_start, b, a.n_rows, a.max_nodes, s.row0, s.n, a.err);
+  s.ctx = 0;
+  if (s.seq < 0 || s.seq >= a.n_seqs) {
+    atomicOr(a.err, ERR_BAD_INDEX);
+    s.seq = 0;
+  } else {
+    s.ctx = a.len[s.seq];
+    if (s.ctx < 0 || s.ctx > ((long long)a.max_pages << a.page_shift)) {
+      atomicOr(a.err, ERR_BAD_INDEX);
+      s.ctx = 0;
+    }
+  }
+  s.tiles = s.n ? (s.ctx + KT - 1) / KT + (s.n + KT - 1) / KT : 0;
+  s.nm = (s.n * a.G + kTaRows - 1) / kTaRows;
+  s.base = 0;
+  return s;
+}
+
+// Sums over a CTA of NW warps: every thread's v before it, and the total.
+template <int NW>
+QHL_DEV long long ta_scan(long long v, long long* scratch, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    if (i < warp) before += scratch[i];
+    total += scratch[i];
+  }
+  return before + inc - v;
+}
+
+// The groups, from the units with an M tile per segment (`alone`) and with all of
+// a tree's (`together`), over all KV heads.
+QHL_DEV TaHead ta_head(long long alone, long long together, int nm, int grid, int Hkv) {
+  TaHead h;
+  const int groups = nm ? grid / nm : 0;
+  const bool shared = nm > 1 && groups > 0 && together * grid * 20 <= alone * groups * 23;
+  h.tiles = (short)(shared ? nm : 1);
+  h.heads = 1;
+  for (int x = 2; x <= Hkv; ++x)
+    if (Hkv % x == 0 && grid / (x * h.tiles) * (x * h.tiles) * 20 >= grid * 19) h.heads = (short)x;
+  h.units = (shared ? together : alone) / h.heads;
+  h.runs = (int)min((long long)(grid / (h.heads * h.tiles)), h.units);
+  return h;
+}
+
+// The plan, by all threads of a CTA of NW warps: every tree to `out`, with its
+// first unit.  Trees are taken 32 NW at a time.
+template <int KT, int NW>
+QHL_DEV TaHead ta_plan(const TaArgs& a, TaSeq* out, long long* scratch) {
+  const int tid = threadIdx.x;
+  long long alone = 0, together = 0;
+  int nm = 0;
+  for (int b = tid; b < a.n_batch; b += 32 * NW) {
+    const TaSeq s = ta_seq<KT>(a, b);
+    out[b] = s;
+    alone += (long long)a.Hkv * s.nm * ta_units(s);
+    together += (long long)a.Hkv * ta_units(s);
+    nm = max(nm, s.nm);
+  }
+  long long all_alone, all_together, total;
+  ta_scan<NW>(alone, scratch, all_alone);
+  ta_scan<NW>(together, scratch, all_together);
+  nm = __reduce_max_sync(0xffffffffu, nm);
+  __syncthreads();
+  if ((tid & 31) == 0) scratch[tid >> 5] = nm;
+  __syncthreads();
+  for (int i = 0; i < NW; ++i) nm = max(nm, (int)scratch[i]);
+  const TaHead h = ta_head(all_alone, all_together, nm, a.grid, a.Hkv);
+  long long base = 0;
+  for (int b0 = 0; b0 < a.n_batch; b0 += 32 * NW) {
+    const int b = b0 + tid;
+    const long long mine = b < a.n_batch ? (long long)ta_segments(out[b], h, a.Hkv) * ta_units(out[b]) : 0;
+    const long long at = base + ta_scan<NW>(mine, scratch, total);
+    if (b < a.n_batch) out[b].base = at;
+    base += total;
+  }
+  __syncthreads();
+  return h;
+}
+
+// The plan of a large batch.
 template <int DIM>
 __global__ void __launch_bounds__(512) tree_plan_kernel(const __grid_constant__ TaArgs a) {
-  constexpr int KT = TaShape<DIM>::KT;
-  __shared__ int s_nt[kMaxBatch], s_nm[kMaxBatch], s_end[kMaxBatch];
-  __shared__ int s_w[2][16];
-  __shared__ int s_lc[kTaWaves];
-  __shared__ long long s_cost[kTaWaves];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) pdl_launch();
-  int longest = 0, whole = 0;
-  for (int b = tid; b < a.n_batch; b += 512) {
-    TaSeq s;
-    tree_rows(a.q_start, b, a.n_rows, a.max_nodes, s.row0, s.n, a.err);
-    s.seq = __ldg(a.seq + b);
-    s.ctx = 0;
-    if (s.seq < 0 || s.seq >= a.n_seqs) {
-      atomicOr(a.err, ERR_BAD_INDEX);
-      s.seq = 0;
-    } else {
-      s.ctx = a.len[s.seq];
-      if (s.ctx < 0 || s.ctx > ((long long)a.max_pages << a.page_shift)) {
-        atomicOr(a.err, ERR_BAD_INDEX);
-        s.ctx = 0;
-      }
-    }
-    s.tiles = s.n ? (s.ctx + KT - 1) / KT + (s.n + KT - 1) / KT : 0;
-    s.chunks = s.slot0 = s.pad = 0;
-    const int nm = (s.n * a.G + kTaRows - 1) / kTaRows;
-    a.seqs[b] = s;
-    s_nt[b] = s.tiles;
-    s_nm[b] = nm * a.Hkv;
-    longest = max(longest, s.tiles);
-    whole += nm * a.Hkv;
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  whole = __reduce_add_sync(0xffffffffu, whole);
-  if (lane == 0) {
-    s_w[0][warp] = longest;
-    s_w[1][warp] = whole;
-  }
-  __syncthreads();
-  longest = whole = 0;
-  for (int i = 0; i < 16; ++i) {
-    longest = max(longest, s_w[0][i]);
-    whole += s_w[1][i];
-  }
-  // Warp w: the fewest tiles per item such that the items fit w0 + w waves of
-  // the grid (w0: the fewest waves possible) and the split ones the workspace;
-  // its cost in tiles, with about two tiles' time for an item's start and end.
-  const int w0 = (whole + a.grid - 1) / a.grid;
-  if (warp < kTaWaves) {
-    int lo = 1, hi = max(longest, 1);
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      int items = 0, split = 0;
-      for (int b = lane; b < a.n_batch; b += 32) {
-        const int x = (s_nt[b] + mid - 1) / mid * s_nm[b];
-        items += min(x, 1 << 20);
-        split += s_nt[b] > mid ? min(x, 1 << 20) : 0;
-      }
-      items = __reduce_add_sync(0xffffffffu, items);
-      split = __reduce_add_sync(0xffffffffu, split);
-      if (items >= 0 && split >= 0 && items <= (w0 + warp) * a.grid && split <= kTaSplitItems * a.grid)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    if (lane == 0) {
-      s_lc[warp] = lo;
-      s_cost[warp] = (long long)max(w0 + warp, 1) * (lo + 2);
-    }
-  }
-  __syncthreads();
-  int best = 0;
-  for (int i = 1; i < kTaWaves; ++i)
-    if (s_cost[i] < s_cost[best]) best = i;
-  const int lc = s_lc[best];
-  // prefix sums of the items and of the partial rows, 512 trees at a time
-  int items = 0, slots = 0;
-  for (int base = 0; base < a.n_batch; base += 512) {
-    const int b = base + tid;
-    int x = 0, y = 0, chunks = 0;
-    if (b < a.n_batch) {
-      chunks = (s_nt[b] + lc - 1) / lc;
-      x = chunks * s_nm[b];
-      y = chunks > 1 ? chunks * a.Hkv * a.seqs[b].n * a.G : 0;
-    }
-    int ix = x, iy = y;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, ix, o), v = __shfl_up_sync(0xffffffffu, iy, o);
-      if (lane >= o) {
-        ix += u;
-        iy += v;
-      }
-    }
-    __syncthreads();
-    if (lane == 31) {
-      s_w[0][warp] = ix;
-      s_w[1][warp] = iy;
-    }
-    __syncthreads();
-    int tx = 0, ty = 0;
-    for (int i = 0; i < 16; ++i) {
-      if (i == warp) {
-        ix += tx;
-        iy += ty;
-      }
-      tx += s_w[0][i];
-      ty += s_w[1][i];
-    }
-    if (b < a.n_batch) {
-      s_end[b] = items + ix;
-      a.seqs[b].chunks = chunks;
-      a.seqs[b].slot0 = slots + iy - y;
-    }
-    items += tx;
-    slots += ty;
-  }
-  __syncthreads();
-  if (tid == 0) a.hdr[0] = items;
-  for (int i = tid; i < items; i += 512) {
-    int lo = 0, hi = a.n_batch - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (s_end[mid] > i) hi = mid;
-      else lo = mid + 1;
-    }
-    const int nt = s_nt[lo], chunks = (nt + lc - 1) / lc, nm = s_nm[lo] / a.Hkv;
-    int r = i - (s_end[lo] - chunks * s_nm[lo]);
-    const int mt = r % nm;
-    r /= nm;
-    const int h = r % a.Hkv, ck = r / a.Hkv;
-    a.items[i] = make_int4(lo, (int)((long long)ck * nt / chunks), (int)((long long)(ck + 1) * nt / chunks), h | mt << 8 | ck << 16);
-  }
+  __shared__ long long s_scratch[16];
+  if (threadIdx.x == 0) pdl_launch();
+  pdl_wait();
+  const TaHead h = ta_plan<TaShape<DIM>::KT, 16>(a, a.seqs, s_scratch);
+  if (threadIdx.x == 0) *a.head = h;
 }
 
 // ---------------------------------------------------------------- attention --
@@ -267,27 +264,98 @@ struct TaBars {
   uint64_t q_ready, s_full[2], p_ready[2], pv_done[2], mask_full, mask_empty;
 };
 
+// The plan as a CTA holds it; `seq` only for small batches.
+struct TaOwnPlan {
+  TaSeq seq[kTaOwnPlan];
+  long long scratch[kTaThreads / 32];
+  TaHead head;
+  int first_b;       // the tree that the CTA's run starts in
+};
+
 // What the roles know of an item.
 struct TaItem {
   TaSeq s;
-  int t0, t1, h, ck, mt, nct;   // nct: cache tiles
+  int t0, t1, h, mt, nct;      // nct: cache tiles
+  QHL_DEV bool whole() const { return t0 == 0 && t1 == s.tiles; }
 };
 
+// The items of a CTA, in order.
 template <int DIM>
-QHL_DEV TaItem ta_item(const TaArgs& a, int i) {
-  const int4 it = __ldcg(a.items + i);
-  TaItem r;
-  const int4* s = reinterpret_cast<const int4*>(a.seqs + it.x);
-  const int4 s0 = __ldcg(s), s1 = __ldcg(s + 1);
-  r.s = TaSeq{s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-  r.t0 = it.y;
-  r.t1 = it.z;
-  r.h = it.w & 255;
-  r.ck = it.w >> 16;
-  r.mt = it.w >> 8 & 255;
-  r.nct = (r.s.ctx + TaShape<DIM>::KT - 1) / TaShape<DIM>::KT;
-  return r;
+struct TaCursor {
+  long long u, end;
+  int b, head, mt;             // the tree; the CTA's head and M tile within its group
+
+  QHL_DEV TaCursor(const TaArgs& a, const TaOwnPlan& p) {
+    const int per = p.head.heads * p.head.tiles, run = (int)blockIdx.x / per, j = (int)blockIdx.x % per;
+    head = j / p.head.tiles;
+    mt = j % p.head.tiles;
+    u = end = 0;
+    b = p.first_b;
+    if (run < p.head.runs) {
+      u = ta_run_start(p.head.units, p.head.runs, run);
+      end = ta_run_start(p.head.units, p.head.runs, run + 1);
+    }
+  }
+  QHL_DEV bool next(const TaArgs& a, const TaOwnPlan& p, TaItem& w) {
+    while (u < end) {
+      if (a.n_batch <= kTaOwnPlan) {
+        w.s = p.seq[b];
+      } else {
+        const int4* s = reinterpret_cast<const int4*>(a.seqs + b);
+        const int4 s0 = __ldcg(s), s1 = __ldcg(s + 1);
+        w.s = TaSeq{s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, (long long)(unsigned)s1.z | (long long)s1.w << 32};
+      }
+      const int units = ta_units(w.s);
+      const long long at = u - w.s.base;
+      if (at >= (long long)ta_segments(w.s, p.head, a.Hkv) * units) {                      // behind its last segment, or it has none
+        ++b;
+        continue;
+      }
+      const int seg = (int)(at / units), x = (int)(at - (long long)seg * units);
+      const int y = (int)min((long long)units, x + (end - u));
+      u += y - x;
+      w.t0 = max(0, x - kTaStart);
+      w.t1 = max(0, y - kTaStart);
+      const bool shared = p.head.tiles > 1;
+      w.h = (shared ? seg : seg / w.s.nm) * p.head.heads + head;
+      w.mt = shared ? mt : seg % w.s.nm;
+      w.nct = (w.s.ctx + TaShape<DIM>::KT - 1) / TaShape<DIM>::KT;
+      if (w.t1 > w.t0 && w.mt < w.s.nm) return true;
+    }
+    return false;
+  }
+};
+
+// Every CTA's plan (all threads).  CTA 0 of a small batch leaves it for the join.
+template <int DIM>
+QHL_DEV void ta_own_plan(const TaArgs& a, TaOwnPlan& p) {
+  const int tid = threadIdx.x;
+  const bool own = a.n_batch <= kTaOwnPlan;
+  if (own) {
+    const TaHead h = ta_plan<TaShape<DIM>::KT, kTaThreads / 32>(a, p.seq, p.scratch);
+    if (tid == 0) p.head = h;
+    if (blockIdx.x == 0) {
+      if (tid == 0) *a.head = h;
+      if (tid < a.n_batch) a.seqs[tid] = p.seq[tid];
+    }
+  } else if (tid == 0) {
+    const int4 h = __ldcg(reinterpret_cast<const int4*>(a.head));
+    p.head = TaHead{(long long)(unsigned)h.x | (long long)h.y << 32, h.z, (short)(h.w & 0xffff), (short)(h.w >> 16)};
+  }
+  if (tid == 0) p.first_b = 0;
+  __syncthreads();
+  const int run = (int)blockIdx.x / (p.head.heads * p.head.tiles);
+  const long long u = run < p.head.runs ? ta_run_start(p.head.units, p.head.runs, run) : -1;
+  for (int b = tid; b < a.n_batch; b += kTaThreads) {
+    const TaSeq s = own ? p.seq[b] : a.seqs[b];
+    if (s.base <= u && u < s.base + (long long)ta_segments(s, p.head, a.Hkv) * ta_units(s)) p.first_b = b;
+  }
+  __syncthreads();
 }
+
+// Partial row of row r of an M tile's part that CTA `cta` computed; `on`: the part
+// goes on from the CTA before.
+QHL_DEV long long ta_slot(const TaArgs& a, int cta, bool on, int r) { return ((long long)cta * 2 + (on ? 0 : 1)) * a.slot_rows + r; }
 
 // Rows of V that the product of a tile needs: its keys, up to a multiple of 16.
 template <int KT>
@@ -299,6 +367,7 @@ template <int DIM, bool BF16>
 __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_constant__ TaArgs a) {
   using Sh = TaShape<DIM>;
   constexpr int KT = Sh::KT, CH = Sh::CH, NS = Sh::NS, HK = KT / 2;
+  static_assert(NS % 2 == 0, "K has the even slots, V the odd ones");
   extern __shared__ uint8_t smem_raw[];
   __shared__ TaBars bars;
   __shared__ uint32_t s_tmem;
@@ -306,13 +375,13 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
   __shared__ int s_jump[kMaxNodes];
   __shared__ unsigned s_bad[4];                      // tokens whose V row holds an infinity or NaN
   __shared__ float s_max[2][2][kTaRows], s_sum[2][kTaRows];
+  __shared__ __align__(16) TaOwnPlan s_plan;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   auto bar = [](const uint64_t& b) { return smem_u32(&b); };
 
   if (tid == 0) {
-    pdl_launch();
     for (int i = 0; i < NS; ++i) {
       mbar_init(bar(bars.full[i]), 1);
       mbar_init(bar(bars.empty[i]), 1);
@@ -337,9 +406,11 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   pdl_wait();
-  const int n_items = __ldcg(a.hdr);
+  ta_own_plan<DIM>(a, s_plan);
+  TaCursor<DIM> cursor(a, s_plan);
+  TaItem item;
   // Every wait is bounded; a role that gave one up stops (ok = false) once those
   // it shares a named barrier with know it too.
   bool ok = true;
@@ -355,8 +426,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
     uint32_t r = 0;
     const int pchunks = a.box == KT ? 1 : CH, dchunks = a.dbox == KT ? 1 : CH;
     const int pbox = lane / pchunks, pchunk = lane % pchunks, boxes_per_tile = KT >> a.box_shift;
-    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      const TaItem w = ta_item<DIM>(a, i);
+    while (ok && cursor.next(a, s_plan, item)) {
+      const TaItem w = item;
       const int* row = a.table + (size_t)w.s.seq * a.max_pages;
       // page numbers of this item's boxes, 32 at a time, one batch ahead
       const int box_end = (w.s.ctx + a.box - 1) >> a.box_shift;
@@ -408,61 +479,76 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
     // The two products have an issuer each: a wait that is over still takes some
     // 250 cycles under load, and one thread's waits for both left the tensor core
     // idle for 40% of a tile (2400 cycles instead of 1450 at 256 dimensions).
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_f16(BF16, false, kTaRows, KT);
-      uint32_t r = 0, T = 0, it = 0;
-      for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x, ++it) {
-        const int4 w = __ldcg(a.items + i);
-        if (!(ok = mbar_wait(bar(bars.q_ready), it & 1, a.err, kTaWait))) break;
-        for (int tile = w.y; tile < w.z; ++tile, ++T, r += 2) {
-          const uint32_t s = r % NS, b = T & 1;
-          if (!(ok = mbar_wait(bar(bars.full[s]), r / NS & 1, a.err, kTaWait))) break;
-          // p of the tile before last, which lies in this S, is used
-          if (T >= 2 && !(ok = mbar_wait(bar(bars.pv_done[b]), (T >> 1 & 1) ^ 1, a.err, kTaWait))) break;
-          tc_fence_after();
-          const uint64_t kd = smem_desc_sw128(ring + s * Sh::SLOT, 16);
+    // The whole warp walks the tiles, with values that the compiler knows to be the
+    // same in all lanes, and one lane issues: the descriptors then stay in uniform
+    // registers (from one lane's own loop a product took 1.2 x as long to issue).
+    constexpr uint32_t id = idesc_f16(BF16, false, kTaRows, KT);
+    uint32_t slot = 0, phase = 0, T = 0, it = 0;
+    for (; ok && cursor.next(a, s_plan, item); ++it) {
+      const int n = __shfl_sync(0xffffffffu, item.t1 - item.t0, 0);
+      if (!(ok = wait_warp(bars.q_ready, it & 1))) break;
+      for (int i = 0; i < n; ++i, ++T) {
+        const uint32_t b = T & 1;
+        if (!(ok = wait_warp(bars.full[slot], phase))) break;
+        // p of the tile before last, which lies in this S, is used
+        if (T >= 2 && !(ok = wait_warp(bars.pv_done[b], (T >> 1 & 1) ^ 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t kd = smem_desc_sw128(ring + slot * Sh::SLOT, 16);
 #pragma unroll
           for (int k = 0; k < DIM / 16; ++k)
             mma_f16_ts(tmem + Sh::S0 + b * KT, tmem + Sh::Q0 + k * 8, kd + (uint64_t)((k / 4) * (KT * 128) + (k % 4) * 32 >> 4), id, k != 0);
           tc_commit(&bars.s_full[b]);
-          tc_commit(&bars.empty[s]);
+          tc_commit(&bars.empty[slot]);
+        }
+        __syncwarp();
+        slot += 2;                                   // K has the even slots
+        if (slot == NS) {
+          slot = 0;
+          phase ^= 1;
         }
       }
     }
-    __syncwarp();
   } else if (warp == 10) {
     // ------------------------------------------------------------ O += p V --
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_f16(BF16, true, kTaRows, DIM);
-      uint32_t r = 1, T = 0, vok_phase = 0;
-      for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-        const TaItem w = ta_item<DIM>(a, i);
-        for (int tile = w.t0; tile < w.t1; ++tile, ++T, r += 2) {
-          const uint32_t s = r % NS, b = T & 1;
-          const int keys = ta_keys<KT>(w, tile);
-          if (!(ok = mbar_wait(bar(bars.full[s]), r / NS & 1, a.err, kTaWait))) break;
-          if (tile >= w.nct || keys < KT) {
-            if (!(ok = mbar_wait(bar(bars.vok[s]), vok_phase >> s & 1, a.err, kTaWait))) break;
-            vok_phase ^= 1u << s;
-          }
-          if (!(ok = mbar_wait(bar(bars.p_ready[b]), T >> 1 & 1, a.err, kTaWait))) break;
-          tc_fence_after();
+    constexpr uint32_t id = idesc_f16(BF16, true, kTaRows, DIM);
+    uint32_t slot = 1, phase = 0, T = 0, vok_phase = 0;
+    while (ok && cursor.next(a, s_plan, item)) {
+      const int t0 = __shfl_sync(0xffffffffu, item.t0, 0), t1 = __shfl_sync(0xffffffffu, item.t1, 0);
+      const int nct = __shfl_sync(0xffffffffu, item.nct, 0), ctx = __shfl_sync(0xffffffffu, item.s.ctx, 0);
+      const int nodes = __shfl_sync(0xffffffffu, item.s.n, 0);
+      for (int tile = t0; tile < t1; ++tile, ++T) {
+        const uint32_t b = T & 1;
+        const int keys = tile >= nct ? min(KT, nodes - (tile - nct) * KT) : min(KT, ctx - tile * KT);
+        if (!(ok = wait_warp(bars.full[slot], phase))) break;
+        if (tile >= nct || keys < KT) {
+          if (!(ok = wait_warp(bars.vok[slot], vok_phase >> slot & 1))) break;
+          vok_phase ^= 1u << slot;
+        }
+        if (!(ok = wait_warp(bars.p_ready[b], T >> 1 & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
           const uint32_t p = tmem + Sh::S0 + b * KT;
-          const uint64_t vd = smem_desc_sw128(ring + s * Sh::SLOT, KT * 128);
+          const uint64_t vd = smem_desc_sw128(ring + slot * Sh::SLOT, KT * 128);
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            if (16 * k < keys) mma_f16_ts(tmem, p + k * 8, vd + (uint64_t)(k * 2048 >> 4), id, tile != w.t0 || k);
+            if (16 * k < keys) mma_f16_ts(tmem, p + k * 8, vd + (uint64_t)(k * 2048 >> 4), id, tile != t0 || k);
           tc_commit(&bars.pv_done[b]);
-          tc_commit(&bars.empty[s]);
+          tc_commit(&bars.empty[slot]);
+        }
+        __syncwarp();
+        slot += 2;
+        if (slot > NS) {
+          slot = 1;
+          phase ^= 1;
         }
       }
     }
-    __syncwarp();
   } else if (warp == 11) {
     // ------------------------------------------- masks, tiles that need care --
     uint32_t r = 1, it = 0;
-    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x, ++it) {
-      const TaItem w = ta_item<DIM>(a, i);
+    for (; ok && cursor.next(a, s_plan, item); ++it) {
+      const TaItem w = item;
       const int n = w.s.n;
       if (it && !(ok = wait_warp(bars.mask_empty, (it - 1) & 1))) break;
       if (lane < 4) s_bad[lane] = 0;
@@ -555,8 +641,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
     const uint32_t lanes = (uint32_t)(qd * 32) << 16;
     const float c = a.c, thr = 8.f / c;
     uint32_t T = 0, it = 0;
-    for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++it) {
-      const TaItem w = ta_item<DIM>(a, i);
+    for (; cursor.next(a, s_plan, item); ++it) {
+      const TaItem w = item;
       const int qr = w.mt * kTaRows + row, node = qr / a.G, g = qr - node * a.G;   // the thread's token and query head
       const bool valid = node < w.s.n;
       const bool active = __any_sync(0xffffffffu, valid);
@@ -608,7 +694,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
                 if (!(bits >> e & 1)) sv[j][e] = 0xff800000u;
             }
           } else {
-            const int lim = alive || !valid ? w.s.ctx - tile * KT - hf * HK : 0;
+            const int lim = w.s.ctx - tile * KT - hf * HK;
             if (lim < HK) {
 #pragma unroll
               for (int j = 0; j < HK / 32; ++j)
@@ -654,21 +740,21 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
             }
           }
           const float ms = m == -INFINITY ? 0.f : m * c;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float2 c2 = make_float2(c, c), ms2 = make_float2(-ms, -ms);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int j = 0; j < HK / 32; ++j) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float p0 = ex2(__fmaf_rn(__uint_as_float(sv[j][e]), c, -ms));
-              const float p1 = ex2(__fmaf_rn(__uint_as_float(sv[j][e + 1]), c, -ms));
-              sum[e & 2] += p0;
-              sum[(e & 2) + 1] += p1;
-              pk[e / 2] = pack2<BF16>(p0, p1);
+              const float2 x = ffma2(make_float2(__uint_as_float(sv[j][e]), __uint_as_float(sv[j][e + 1])), c2, ms2);
+              const float2 y = make_float2(ex2(x.x), ex2(x.y));
+              sum[e >> 1 & 1] = __fadd2_rn(sum[e >> 1 & 1], y);
+              pk[e / 2] = pack2<BF16>(y.x, y.y);
             }
             tmem_st16(sb + hf * (KT / 4) + 16 * j, pk);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_st_wait();
           tc_fence_before();
         }
@@ -686,8 +772,12 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
         ok = bar_and(1 + qd, 64, ok);
         if (!ok) break;
         l += s_sum[hf ^ 1][row];
-        const bool whole = w.s.chunks == 1;
-        const long long slot = w.s.slot0 + ((long long)w.ck * a.Hkv + w.h) * w.s.n * a.G + (long long)node * a.G + g;
+        if (!alive) {                                // padded: whatever was summed, nothing was seen
+          m = -INFINITY;
+          l = 0.f;
+        }
+        const bool whole = w.whole();
+        const long long slot = ta_slot(a, blockIdx.x, w.t0 > 0, row);
         const float inv = l > 0.f || l != l ? __frcp_rn(l) : 0.f;
         const bool none = l == 0.f;                  // nothing seen: 0, whatever the tiles held
         uint32_t bad[4];
@@ -751,6 +841,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
       if (lane == 0) mbar_arrive(bar(bars.mask_empty));
     }
   }
+  // The join's CTAs come only now: waiting beside this one they slowed it by 10%.
+  if (tid == 0) pdl_launch();
   if (!ok) drain_inflight_copies();
   tc_fence_before();
   __syncthreads();
@@ -762,73 +854,110 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
 
 // --------------------------------------------------------------------- join --
 
-// One CTA per (query head, token, tree): the ranges' partials, in their order
-// within each of four groups, and the groups as (0 + 1) + (2 + 3).
-template <int DIM, bool BF16>
-__global__ void __launch_bounds__(DIM) tree_join_kernel(const __grid_constant__ TaArgs a) {
-  constexpr int L = DIM / 4;                         // threads per group, four values each
-  __shared__ float s_wt[kTaSplitItems * 256];
-  __shared__ float s_red[DIM / 32];
-  __shared__ float4 s_o[4][L];
-  const int qh = blockIdx.x, node = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  pdl_wait();
-  const int4* sp = reinterpret_cast<const int4*>(a.seqs + b);
-  const int4 s0 = __ldcg(sp), s1 = __ldcg(sp + 1);
-  const int n = s0.y, chunks = s1.x;
-  if (node >= n || chunks <= 1) return;
-  const int h = qh / a.G, g = qh - h * a.G;
-  const long long step = (long long)a.Hkv * n * a.G;
-  const long long slot = s1.y + (long long)h * n * a.G + (long long)node * a.G + g;
-  float top = -INFINITY;
-  for (int j = tid; j < chunks; j += DIM) {
-    const float2 ml = __ldcg(a.pml + slot + j * step);
-    if (ml.y != 0.f) top = fmaxf(top, ml.x);
-  }
-  top = warp_max(top);
-  if ((tid & 31) == 0) s_red[tid >> 5] = top;
-  __syncthreads();
-  top = s_red[0];
-  for (int j = 1; j < DIM / 32; ++j) top = fmaxf(top, s_red[j]);
-  float sum = 0.f;
-  for (int j = tid; j < chunks; j += DIM) {
-    const float2 ml = __ldcg(a.pml + slot + j * step);
-    const float wt = ml.y != 0.f ? ex2(ml.x - top) : 0.f;   // NaN counts
-    s_wt[j] = ml.y != 0.f ? wt : -1.f;               // -1: a range that saw nothing, not read
-    sum += wt * ml.y;
-  }
-  sum = warp_sum(sum);
-  __syncthreads();
-  if ((tid & 31) == 0) s_red[tid >> 5] = sum;
-  __syncthreads();
-  sum = 0.f;
-  for (int j = 0; j < DIM / 32; ++j) sum += s_red[j];
+// One vector (token, query head) per warp, or per four warps where there are few:
+// then a warp takes every fourth range and the sums meet as (0 + 1) + (2 + 3).
+// Within a warp the ranges are added in their order, 32 weights at a time.
+constexpr int kJoinFew = 148 * 16;   // vectors up to which four warps share one
 
-  const int grp = tid / L, l = tid % L;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* po = reinterpret_cast<const float4*>(a.po + slot * DIM) + l;
-#pragma unroll 8
-  for (int j = grp; j < chunks; j += 4) {
-    const float4 x = __ldcg(po + j * step * L);
-    const float wt = s_wt[j];
-    if (wt != -1.f) {
-      o.x = fmaf(wt, x.x, o.x);
-      o.y = fmaf(wt, x.y, o.y);
-      o.z = fmaf(wt, x.z, o.z);
-      o.w = fmaf(wt, x.w, o.w);
+template <int DIM, bool BF16, int W>
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TaArgs a) {
+  constexpr int E = DIM / 32;                        // elements per lane
+  __shared__ float s_o[8][DIM + 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
+  const int Hq = a.Hkv * a.G;
+  const long long v = (long long)blockIdx.x * (8 / W) + warp / W;
+  if (threadIdx.x == 0) pdl_launch();
+  pdl_wait();
+  const int qh = (int)(v % Hq), node = (int)(v / Hq % a.max_nodes);
+  const long long b = v / Hq / a.max_nodes;
+  int chunks = 0, row0 = 0, cta0 = 0, per = 1;       // the CTAs that have a part of it: cta0 + j * per
+  if (b < a.n_batch) {
+    const int4* sp = reinterpret_cast<const int4*>(a.seqs + b);
+    const int4 s0 = __ldcg(sp), s1 = __ldcg(sp + 1), h0 = __ldcg(reinterpret_cast<const int4*>(a.head));
+    row0 = s0.x;
+    if (node < s0.y) {
+      const long long units = (long long)(unsigned)h0.x | (long long)h0.y << 32;
+      const int runs = h0.z, h = qh / a.G, mt = (node * a.G + qh - h * a.G) / kTaRows;
+      const int heads = h0.w & 0xffff, tiles = h0.w >> 16, seg = tiles > 1 ? h / heads : h / heads * s1.y + mt;
+      const long long u0 = ((long long)(unsigned)s1.z | (long long)s1.w << 32) + (long long)seg * (s1.x + kTaStart);
+      const int r0 = ta_run_of(units, runs, u0 + kTaStart), r1 = ta_run_of(units, runs, u0 + s1.x + kTaStart - 1);
+      per = heads * tiles;
+      cta0 = r0 * per + h % heads * tiles + (tiles > 1 ? mt : 0);
+      chunks = r1 - r0 + 1;
     }
   }
-  s_o[grp][l] = o;
-  __syncthreads();
-  if (grp == 0) {
-    const float4 p = s_o[1][l], q = s_o[2][l], r = s_o[3][l];
-    const float inv = sum > 0.f || sum != sum ? __frcp_rn(sum) : 0.f;
-    const float x = ((o.x + p.x) + (q.x + r.x)) * inv, y = ((o.y + p.y) + (q.y + r.y)) * inv;
-    const float z = ((o.z + p.z) + (q.z + r.z)) * inv, u = ((o.w + p.w) + (q.w + r.w)) * inv;
-    uint8_t* dst = static_cast<uint8_t*>(a.out) + ((long long)(s0.x + node) * a.out_stride + qh * DIM + 4 * l) * 2;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(x, y), pack2<BF16>(z, u));
-    if (l == 0 && a.lse)
-      a.lse[(long long)(s0.x + node) * (a.Hkv * a.G) + qh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  const bool mine = chunks > 1;
+  float o[E], top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  if (mine) {
+    const int r = (node * a.G + qh % a.G) % kTaRows;
+    auto slot = [&](int j) { return ta_slot(a, cta0 + j * per, j > 0, r); };
+    for (int j = lane; j < chunks; j += 32) {
+      const float2 ml = __ldcg(a.pml + slot(j));
+      if (ml.y != 0.f) top = fmaxf(top, ml.x);
+    }
+    top = warp_max(top);
+    const float* po = a.po + lane * E;
+    for (int j0 = part; j0 < chunks; j0 += 32 * W) {
+      const int jl = j0 + lane * W;
+      float wt = 0.f;                                // 0: a range that saw nothing, not read
+      if (jl < chunks) {
+        const float2 ml = __ldcg(a.pml + slot(jl));
+        if (ml.y != 0.f) {
+          wt = ex2(ml.x - top);                      // NaN counts
+          sum += wt * ml.y;
+        }
+      }
+      const int m = min(32, (chunks - j0 + W - 1) / W);
+      constexpr int U = E == 8 ? 4 : 8;              // ranges whose loads are in flight together
+      for (int k = 0; k < m; k += U) {
+        float y[U][E];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float* x = po + slot(j0 + min(k + u, m - 1) * W) * DIM;
+          if constexpr (E >= 4) {
+#pragma unroll
+            for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(&y[u][e]) = __ldcg(reinterpret_cast<const float4*>(x + e));
+          } else {
+            *reinterpret_cast<float2*>(&y[u][0]) = __ldcg(reinterpret_cast<const float2*>(x));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float w = __shfl_sync(0xffffffffu, wt, (k + u) & 31);
+          if (k + u < m && w != 0.f)                 // what an empty range left is not used
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(w, y[u][e], o[e]);
+        }
+      }
+    }
+    sum = warp_sum(sum);
   }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
+    if (lane == 0) s_o[warp][DIM] = sum;
+    __syncthreads();
+    if (!mine || part) return;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      o[e] = (s_o[warp][e * 32 + lane] + s_o[warp + 1][e * 32 + lane]) + (s_o[warp + 2][e * 32 + lane] + s_o[warp + 3][e * 32 + lane]);
+    sum = (s_o[warp][DIM] + s_o[warp + 1][DIM]) + (s_o[warp + 2][DIM] + s_o[warp + 3][DIM]);
+  }
+  if (!mine) return;
+  const float inv = sum > 0.f || sum != sum ? __frcp_rn(sum) : 0.f;
+  uint32_t r[E / 2];
+#pragma unroll
+  for (int e = 0; e < E; e += 2) r[e / 2] = pack2<BF16>(o[e] * inv, o[e + 1] * inv);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (long long)(row0 + node) * a.out_stride + qh * DIM) + lane * (E / 2);
+  if constexpr (E == 8)
+    *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
+  else if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(r[0], r[1]);
+  else
+    *dst = r[0];
+  if (lane == 0 && a.lse) a.lse[(long long)(row0 + node) * Hq + qh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
 // --------------------------------------------------------------------- host --
@@ -847,9 +976,20 @@ std::mutex g_ta_mu;
 TaDevice g_ta[64];
 EncodeFn g_encode = nullptr;
 
+// The full shared-memory carveout for every kernel of the chain: an SM that has
+// another split must drain before a CTA of tree_attn_kernel starts there.
+template <typename K>
+cudaError_t full_carveout(K k) {
+  return cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+}
 template <int DIM, bool BF16>
 cudaError_t ta_attributes() {
-  return cudaFuncSetAttribute(tree_attn_kernel<DIM, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, TaShape<DIM>::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<DIM, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, TaShape<DIM>::SMEM);
+  if (e == cudaSuccess) e = full_carveout(tree_attn_kernel<DIM, BF16>);
+  if (e == cudaSuccess) e = full_carveout(tree_join_kernel<DIM, BF16, 1>);
+  if (e == cudaSuccess) e = full_carveout(tree_join_kernel<DIM, BF16, 4>);
+  if (e == cudaSuccess) e = full_carveout(tree_plan_kernel<DIM>);
+  return e;
 }
 
 // SM count and kernel attributes of the current device; the driver's encoder.
@@ -896,20 +1036,19 @@ bool encode(CUtensorMap* m, bool bf16, const void* base, const long long (&dims)
 }
 
 struct TaLayout {
-  size_t seqs, items, pml, po, total;
+  size_t seqs, pml, po, total;
+  int slot_rows;
 };
 
-TaLayout ta_layout(int dim, int Hkv, int G, int n_batch, int max_nodes, int grid) {
-  const long long nm = (max_nodes * G + kTaRows - 1) / kTaRows;
-  const long long items = (long long)n_batch * Hkv * nm + (long long)grid * kTaWaves;
-  const long long rows = (long long)grid * kTaSplitItems * std::min(kTaRows, max_nodes * G);
+TaLayout ta_layout(int dim, int G, int n_batch, int max_nodes, int grid) {
   TaLayout l;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  l.slot_rows = std::min(kTaRows, max_nodes * G);
+  const size_t rows = (size_t)grid * 2 * l.slot_rows;
   l.seqs = 256;
-  l.items = l.seqs + up(sizeof(TaSeq) * (size_t)n_batch);
-  l.pml = l.items + up(16 * (size_t)items);
-  l.po = l.pml + up(8 * (size_t)rows);
-  l.total = l.po + up(4 * (size_t)rows * dim);
+  l.pml = l.seqs + up(sizeof(TaSeq) * (size_t)n_batch);
+  l.po = l.pml + up(8 * rows);
+  l.total = l.po + up(4 * rows * dim);
   return l;
 }
 
@@ -928,10 +1067,14 @@ int ta_check(const char* me, const qhl_kv_pages* kv, int Hq, int n_rows, int n_b
 
 template <int DIM, bool BF16>
 cudaError_t ta_launch(const TaArgs& a, int Hq, cudaStream_t s) {
-  cudaError_t e = launch_ex(tree_plan_kernel<DIM>, dim3(1), dim3(512), 0, s, false, a);
+  // each kernel waits for the one before it on the stream before it reads anything
+  cudaError_t e = cudaSuccess;
+  if (a.n_batch > kTaOwnPlan) e = launch_ex(tree_plan_kernel<DIM>, dim3(1), dim3(512), 0, s, true, a);
   if (e == cudaSuccess) e = launch_ex(tree_attn_kernel<DIM, BF16>, dim3(a.grid), dim3(kTaThreads), TaShape<DIM>::SMEM, s, true, a);
-  if (e == cudaSuccess) e = launch_ex(tree_join_kernel<DIM, BF16>, dim3(Hq, a.max_nodes, a.n_batch), dim3(DIM), 0, s, true, a);
-  return e;
+  if (e != cudaSuccess) return e;
+  const long long vectors = (long long)Hq * a.max_nodes * a.n_batch;
+  if (vectors <= kJoinFew) return launch_ex(tree_join_kernel<DIM, BF16, 4>, dim3((unsigned)((vectors + 1) / 2)), dim3(256), 0, s, true, a);
+  return launch_ex(tree_join_kernel<DIM, BF16, 1>, dim3((unsigned)((vectors + 7) / 8)), dim3(256), 0, s, true, a);
 }
 
 }  // namespace
@@ -951,7 +1094,7 @@ size_t qhl_tree_attention_workspace(const qhl_kv_pages* kv, int n_q_heads, int n
     verify_cuda_err(me, e);
     return 0;
   }
-  return ta_layout(kv->dim, kv->kv_heads, n_q_heads / kv->kv_heads, n_batch, max_nodes, sms).total;
+  return ta_layout(kv->dim, n_q_heads / kv->kv_heads, n_batch, max_nodes, sms).total;
 }
 
 int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_rows, int n_batch, int max_nodes,
@@ -980,7 +1123,7 @@ int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_r
   if (e != cudaSuccess) return verify_cuda_err(me, e);
   const int dim = kv->dim, G = n_q_heads / kv->kv_heads, KT = dim == 256 ? 64 : 128, CH = dim / 64, P = kv->page_rows;
   const bool bf16 = kv->dtype == QHL_BF16;
-  const TaLayout l = ta_layout(dim, kv->kv_heads, G, n_batch, max_nodes, a.grid);
+  const TaLayout l = ta_layout(dim, G, n_batch, max_nodes, a.grid);
   if (workspace_bytes < l.total)
     return verify_err(me, STAGE_E_ARG, "the workspace needs " + std::to_string(l.total) + " bytes");
   a.box = std::min(P, KT);
@@ -1019,9 +1162,9 @@ int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_r
   a.lse = lse_dev;
   a.c = scale * 1.44269504088896340736f;
   uint8_t* ws = static_cast<uint8_t*>(workspace_dev);
-  a.hdr = reinterpret_cast<int*>(ws);
+  a.head = reinterpret_cast<TaHead*>(ws);
   a.seqs = reinterpret_cast<TaSeq*>(ws + l.seqs);
-  a.items = reinterpret_cast<int4*>(ws + l.items);
+  a.slot_rows = l.slot_rows;
   a.pml = reinterpret_cast<float2*>(ws + l.pml);
   a.po = reinterpret_cast<float*>(ws + l.po);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
