@@ -66,15 +66,17 @@ struct TaSeq {
   int row0, n, seq, ctx;
   int tiles;         // key tiles, of the cache and of the drafts
   int nm;            // M tiles per KV head
-  long long base;    // its first unit of work
+  int base;          // its first unit of work
+  int pad;
 };
 
 // The whole plan, for the join and for large batches.
 struct TaHead {
-  long long units;
+  int units;
   int runs;          // none of them empty
-  short heads, tiles;   // KV heads and M tiles of a group of CTAs
+  int heads, tiles;  // KV heads and M tiles of a group of CTAs
 };
+constexpr long long kTaMostUnits = 1LL << 30;
 
 struct TaArgs {
   CUtensorMap k, v;            // cache pages
@@ -99,7 +101,7 @@ struct TaArgs {
   TaHead* head;
   TaSeq* seqs;
   float2* pml;                 // per partial row: c m, l
-  float* po;                   // per partial row: O
+  float* po;                   // per slot: O as [DIM / 4][slot_rows] float4
   int slot_rows;               // partial rows of a slot: an M tile's, or all there can be
   int grid;
   unsigned* err;
@@ -125,9 +127,13 @@ struct TaArgs {
 
 QHL_DEV int ta_segments(const TaSeq& s, const TaHead& h, int Hkv) { return Hkv / h.heads * (h.tiles > 1 ? 1 : s.nm); }
 QHL_DEV int ta_units(const TaSeq& s) { return s.tiles ? s.tiles + kTaStart : 0; }
-// First unit of run r, and the run that has unit u.
-QHL_DEV long long ta_run_start(long long units, int runs, int r) { return units * r / runs; }
-QHL_DEV int ta_run_of(long long units, int runs, long long u) { return (int)(((u + 1) * runs - 1) / units); }
+// First unit of run r, and the run that has unit u: the first units % runs runs
+// have one more.
+QHL_DEV int ta_run_start(const TaHead& h, int r) { return h.units / h.runs * r + min(r, h.units % h.runs); }
+QHL_DEV int ta_run_of(const TaHead& h, int u) {
+  const int q = h.units / h.runs, rem = h.units % h.runs, more = rem * (q + 1);
+  return u < more ? u / (q + 1) : rem + (u - more) / q;
+}
 
 // Tree b, its lengths checked.
 template <int KT>
@@ -148,7 +154,7 @@ QHL_DEV TaSeq ta_seq(const TaArgs& a, int b) {
   }
   s.tiles = s.n ? (s.ctx + KT - 1) / KT + (s.n + KT - 1) / KT : 0;
   s.nm = (s.n * a.G + kTaRows - 1) / kTaRows;
-  s.base = 0;
+  s.base = s.pad = 0;
   return s;
 }
 
@@ -176,17 +182,48 @@ QHL_DEV long long ta_scan(long long v, long long* scratch, long long& total) {
 }
 
 // The groups, from the units with an M tile per segment (`alone`) and with all of
-// a tree's (`together`), over all KV heads.
-QHL_DEV TaHead ta_head(long long alone, long long together, int nm, int grid, int Hkv) {
+// a tree's (`together`), over all KV heads.  A full warp calls it.
+QHL_DEV TaHead ta_head(const TaArgs& a, long long alone, long long together, int nm) {
   TaHead h;
-  const int groups = nm ? grid / nm : 0;
-  const bool shared = nm > 1 && groups > 0 && together * grid * 20 <= alone * groups * 23;
-  h.tiles = (short)(shared ? nm : 1);
-  h.heads = 1;
-  for (int x = 2; x <= Hkv; ++x)
-    if (Hkv % x == 0 && grid / (x * h.tiles) * (x * h.tiles) * 20 >= grid * 19) h.heads = (short)x;
-  h.units = (shared ? together : alone) / h.heads;
-  h.runs = (int)min((long long)(grid / (h.heads * h.tiles)), h.units);
+  const int groups = nm ? a.grid / nm : 0;
+  const bool shared = nm > 1 && groups > 0 && together * a.grid * 20 <= alone * groups * 23;
+  h.tiles = shared ? nm : 1;
+  int best = 1;
+  for (int x = (threadIdx.x & 31) + 1; x <= a.Hkv; x += 32)
+    if (a.Hkv % x == 0 && a.grid / (x * h.tiles) * (x * h.tiles) * 20 >= a.grid * 19) best = x;
+  h.heads = __reduce_max_sync(0xffffffffu, best);
+  long long units = (shared ? together : alone) / h.heads;
+  if (units > kTaMostUnits) {                        // lengths that no cache can have
+    atomicOr(a.err, ERR_BAD_INDEX);
+    units = 0;
+  }
+  h.units = (int)units;
+  h.runs = min(a.grid / (h.heads * h.tiles), h.units);
+  return h;
+}
+
+QHL_DEV long long warp_total(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The plan of at most 32 trees, by one warp: lane b gets tree b.
+template <int KT>
+QHL_DEV TaHead ta_plan_warp(const TaArgs& a, TaSeq& s) {
+  const int lane = threadIdx.x & 31;
+  s = TaSeq{};
+  if (lane < a.n_batch) s = ta_seq<KT>(a, lane);
+  const long long together = (long long)a.Hkv * ta_units(s);
+  const TaHead h = ta_head(a, warp_total(together * s.nm), warp_total(together), __reduce_max_sync(0xffffffffu, s.nm));
+  const int mine = h.units ? ta_segments(s, h, a.Hkv) * ta_units(s) : 0;
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  s.base = inc - mine;
   return h;
 }
 
@@ -212,13 +249,13 @@ QHL_DEV TaHead ta_plan(const TaArgs& a, TaSeq* out, long long* scratch) {
   if ((tid & 31) == 0) scratch[tid >> 5] = nm;
   __syncthreads();
   for (int i = 0; i < NW; ++i) nm = max(nm, (int)scratch[i]);
-  const TaHead h = ta_head(all_alone, all_together, nm, a.grid, a.Hkv);
+  const TaHead h = ta_head(a, all_alone, all_together, nm);
   long long base = 0;
   for (int b0 = 0; b0 < a.n_batch; b0 += 32 * NW) {
     const int b = b0 + tid;
-    const long long mine = b < a.n_batch ? (long long)ta_segments(out[b], h, a.Hkv) * ta_units(out[b]) : 0;
+    const long long mine = h.units && b < a.n_batch ? (long long)ta_segments(out[b], h, a.Hkv) * ta_units(out[b]) : 0;
     const long long at = base + ta_scan<NW>(mine, scratch, total);
-    if (b < a.n_batch) out[b].base = at;
+    if (b < a.n_batch) out[b].base = (int)at;
     base += total;
   }
   __syncthreads();
@@ -282,7 +319,7 @@ struct TaItem {
 // The items of a CTA, in order.
 template <int DIM>
 struct TaCursor {
-  long long u, end;
+  int u, end;
   int b, head, mt;             // the tree; the CTA's head and M tile within its group
 
   QHL_DEV TaCursor(const TaArgs& a, const TaOwnPlan& p) {
@@ -292,8 +329,8 @@ struct TaCursor {
     u = end = 0;
     b = p.first_b;
     if (run < p.head.runs) {
-      u = ta_run_start(p.head.units, p.head.runs, run);
-      end = ta_run_start(p.head.units, p.head.runs, run + 1);
+      u = ta_run_start(p.head, run);
+      end = ta_run_start(p.head, run + 1);
     }
   }
   QHL_DEV bool next(const TaArgs& a, const TaOwnPlan& p, TaItem& w) {
@@ -303,16 +340,15 @@ struct TaCursor {
       } else {
         const int4* s = reinterpret_cast<const int4*>(a.seqs + b);
         const int4 s0 = __ldcg(s), s1 = __ldcg(s + 1);
-        w.s = TaSeq{s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, (long long)(unsigned)s1.z | (long long)s1.w << 32};
+        w.s = TaSeq{s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, 0};
       }
       const int units = ta_units(w.s);
-      const long long at = u - w.s.base;
-      if (at >= (long long)ta_segments(w.s, p.head, a.Hkv) * units) {                      // behind its last segment, or it has none
+      const int at = u - w.s.base;
+      if (at >= ta_segments(w.s, p.head, a.Hkv) * units) {                      // behind its last segment, or it has none
         ++b;
         continue;
       }
-      const int seg = (int)(at / units), x = (int)(at - (long long)seg * units);
-      const int y = (int)min((long long)units, x + (end - u));
+      const int seg = at / units, x = at - seg * units, y = min(units, x + (end - u));
       u += y - x;
       w.t0 = max(0, x - kTaStart);
       w.t1 = max(0, y - kTaStart);
@@ -329,10 +365,30 @@ struct TaCursor {
 // Every CTA's plan (all threads).  CTA 0 of a small batch leaves it for the join.
 template <int DIM>
 QHL_DEV void ta_own_plan(const TaArgs& a, TaOwnPlan& p) {
+  constexpr int KT = TaShape<DIM>::KT;
   const int tid = threadIdx.x;
+  if (a.n_batch <= 32) {
+    if (tid < 32) {
+      TaSeq s;
+      const TaHead h = ta_plan_warp<KT>(a, s);
+      const int run = (int)blockIdx.x / (h.heads * h.tiles), u = run < h.runs ? ta_run_start(h, run) : 0;
+      if (tid < a.n_batch) {
+        p.seq[tid] = s;
+        if (blockIdx.x == 0) a.seqs[tid] = s;
+      }
+      const unsigned here = __ballot_sync(0xffffffffu, s.base <= u && u < s.base + (h.units ? ta_segments(s, h, a.Hkv) * ta_units(s) : 0));
+      if (tid == 0) {
+        p.head = h;
+        p.first_b = here ? __ffs(here) - 1 : 0;
+        if (blockIdx.x == 0) *a.head = h;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   const bool own = a.n_batch <= kTaOwnPlan;
   if (own) {
-    const TaHead h = ta_plan<TaShape<DIM>::KT, kTaThreads / 32>(a, p.seq, p.scratch);
+    const TaHead h = ta_plan<KT, kTaThreads / 32>(a, p.seq, p.scratch);
     if (tid == 0) p.head = h;
     if (blockIdx.x == 0) {
       if (tid == 0) *a.head = h;
@@ -340,15 +396,16 @@ QHL_DEV void ta_own_plan(const TaArgs& a, TaOwnPlan& p) {
     }
   } else if (tid == 0) {
     const int4 h = __ldcg(reinterpret_cast<const int4*>(a.head));
-    p.head = TaHead{(long long)(unsigned)h.x | (long long)h.y << 32, h.z, (short)(h.w & 0xffff), (short)(h.w >> 16)};
+    p.head = TaHead{h.x, h.y, h.z, h.w};
   }
   if (tid == 0) p.first_b = 0;
   __syncthreads();
-  const int run = (int)blockIdx.x / (p.head.heads * p.head.tiles);
-  const long long u = run < p.head.runs ? ta_run_start(p.head.units, p.head.runs, run) : -1;
-  for (int b = tid; b < a.n_batch; b += kTaThreads) {
+  const TaHead h = p.head;
+  const int run = (int)blockIdx.x / (h.heads * h.tiles);
+  const int u = run < h.runs ? ta_run_start(h, run) : -1;
+  for (int b = tid; h.units && b < a.n_batch; b += kTaThreads) {
     const TaSeq s = own ? p.seq[b] : a.seqs[b];
-    if (s.base <= u && u < s.base + (long long)ta_segments(s, p.head, a.Hkv) * ta_units(s)) p.first_b = b;
+    if (s.base <= u && u < s.base + ta_segments(s, h, a.Hkv) * ta_units(s)) p.first_b = b;
   }
   __syncthreads();
 }
@@ -789,7 +846,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
           any_bad |= bad[j] != 0;
         }
         uint8_t* orow = static_cast<uint8_t*>(a.out) + ((long long)(w.s.row0 + node) * a.out_stride + (w.h * a.G + g) * DIM + hf * (DIM / 2)) * 2;
-        float* prow = a.po + slot * DIM + hf * (DIM / 2);
+        float4* prow = reinterpret_cast<float4*>(a.po) + ta_slot(a, blockIdx.x, w.t0 > 0, 0) * (DIM / 4) + row;   // [DIM / 4][slot_rows]
 #pragma unroll 1
         for (int j = 0; j < DIM / 64; ++j) {
           uint32_t o[32];
@@ -824,7 +881,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(prow + 32 * j + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(prow + (long long)(hf * (DIM / 8) + 8 * j + e / 4) * a.slot_rows) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
         if (valid && hf == 0) {
@@ -854,110 +912,105 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
 
 // --------------------------------------------------------------------- join --
 
-// One vector (token, query head) per warp, or per four warps where there are few:
-// then a warp takes every fourth range and the sums meet as (0 + 1) + (2 + 3).
-// Within a warp the ranges are added in their order, 32 weights at a time.
-constexpr int kJoinFew = 148 * 16;   // vectors up to which four warps share one
+// A thread per four values of O; blocks of 256 / W values, each summed by W threads
+// over every W-th part (W = 4 where there are few values), whose sums meet as
+// (0 + 1) + (2 + 3).  The parts of an item lie as [DIM / 4][slot_rows] float4, so
+// that both this kernel and the item's end move whole sectors; the loads of U parts
+// go out together, the weights by a running maximum.
+constexpr long long kJoinFew = 148LL * 1024;   // values (of four) up to which W = 4
 
 template <int DIM, bool BF16, int W>
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TaArgs a) {
-  constexpr int E = DIM / 32;                        // elements per lane
-  __shared__ float s_o[8][DIM + 2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
-  const int Hq = a.Hkv * a.G;
-  const long long v = (long long)blockIdx.x * (8 / W) + warp / W;
-  if (threadIdx.x == 0) pdl_launch();
+__global__ void __launch_bounds__(256, W > 1 ? 3 : 5) tree_join_kernel(const __grid_constant__ TaArgs a) {
+  constexpr int U = W > 1 ? 8 : 4, V = 256 / W;
+  __shared__ float4 s_o[W > 1 ? 256 : 1];
+  __shared__ float2 s_ml[W > 1 ? 256 : 1];
+  const int tid = threadIdx.x, part = tid / V, x = blockIdx.x * V + tid % V;
+  const int b = blockIdx.z, h = blockIdx.y % a.Hkv, mt = blockIdx.y / a.Hkv;
+  if (tid == 0) pdl_launch();
   pdl_wait();
-  const int qh = (int)(v % Hq), node = (int)(v / Hq % a.max_nodes);
-  const long long b = v / Hq / a.max_nodes;
-  int chunks = 0, row0 = 0, cta0 = 0, per = 1;       // the CTAs that have a part of it: cta0 + j * per
-  if (b < a.n_batch) {
-    const int4* sp = reinterpret_cast<const int4*>(a.seqs + b);
-    const int4 s0 = __ldcg(sp), s1 = __ldcg(sp + 1), h0 = __ldcg(reinterpret_cast<const int4*>(a.head));
-    row0 = s0.x;
-    if (node < s0.y) {
-      const long long units = (long long)(unsigned)h0.x | (long long)h0.y << 32;
-      const int runs = h0.z, h = qh / a.G, mt = (node * a.G + qh - h * a.G) / kTaRows;
-      const int heads = h0.w & 0xffff, tiles = h0.w >> 16, seg = tiles > 1 ? h / heads : h / heads * s1.y + mt;
-      const long long u0 = ((long long)(unsigned)s1.z | (long long)s1.w << 32) + (long long)seg * (s1.x + kTaStart);
-      const int r0 = ta_run_of(units, runs, u0 + kTaStart), r1 = ta_run_of(units, runs, u0 + s1.x + kTaStart - 1);
-      per = heads * tiles;
-      cta0 = r0 * per + h % heads * tiles + (tiles > 1 ? mt : 0);
-      chunks = r1 - r0 + 1;
-    }
-  }
-  const bool mine = chunks > 1;
-  float o[E], top = -INFINITY, sum = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  const int4* sp = reinterpret_cast<const int4*>(a.seqs + b);
+  const int4 s0 = __ldcg(sp), s1 = __ldcg(sp + 1), h0 = __ldcg(reinterpret_cast<const int4*>(a.head));
+  const TaHead head{h0.x, h0.y, h0.z, h0.w};
+  if (mt >= s1.y || s1.x == 0 || head.units == 0) return;
+  const int seg = head.tiles > 1 ? h / head.heads : h / head.heads * s1.y + mt;
+  const int u0 = s1.z + seg * (s1.x + kTaStart);
+  const int r0 = ta_run_of(head, u0 + kTaStart), chunks = ta_run_of(head, u0 + s1.x + kTaStart - 1) - r0 + 1;
+  if (chunks <= 1) return;
+  const int per = head.heads * head.tiles, cta0 = r0 * per + h % head.heads * head.tiles + (head.tiles > 1 ? mt : 0);
+  const int cg = x / a.slot_rows, r = x - cg * a.slot_rows, qr = mt * kTaRows + r, node = qr / a.G, g = qr - node * a.G;
+  const bool mine = cg < DIM / 4 && node < s0.y;
+
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float top = -INFINITY, sum = 0.f;
   if (mine) {
-    const int r = (node * a.G + qh % a.G) % kTaRows;
-    auto slot = [&](int j) { return ta_slot(a, cta0 + j * per, j > 0, r); };
-    for (int j = lane; j < chunks; j += 32) {
-      const float2 ml = __ldcg(a.pml + slot(j));
-      if (ml.y != 0.f) top = fmaxf(top, ml.x);
-    }
-    top = warp_max(top);
-    const float* po = a.po + lane * E;
-    for (int j0 = part; j0 < chunks; j0 += 32 * W) {
-      const int jl = j0 + lane * W;
-      float wt = 0.f;                                // 0: a range that saw nothing, not read
-      if (jl < chunks) {
-        const float2 ml = __ldcg(a.pml + slot(jl));
-        if (ml.y != 0.f) {
-          wt = ex2(ml.x - top);                      // NaN counts
-          sum += wt * ml.y;
+    for (int j0 = part; j0 < chunks; j0 += U * W) {
+      float2 ml[U];
+      float4 y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * W;
+        const long long slot = ta_slot(a, cta0 + j * per, j > 0, 0);
+        ml[u] = make_float2(0.f, 0.f);
+        if (j < chunks) {
+          ml[u] = __ldcg(a.pml + slot + r);
+          y[u] = __ldcg(reinterpret_cast<const float4*>(a.po) + slot * (DIM / 4) + x);
         }
       }
-      const int m = min(32, (chunks - j0 + W - 1) / W);
-      constexpr int U = E == 8 ? 4 : 8;              // ranges whose loads are in flight together
-      for (int k = 0; k < m; k += U) {
-        float y[U][E];
+      float now = top;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float* x = po + slot(j0 + min(k + u, m - 1) * W) * DIM;
-          if constexpr (E >= 4) {
+      for (int u = 0; u < U; ++u)
+        if (ml[u].y != 0.f) now = fmaxf(now, ml[u].x);   // a part that saw nothing does not count; NaN does
+      const float al = sum != 0.f ? ex2(top - now) : 0.f;
+      top = now;
+      if (al != 1.f) {
+        sum *= al;
+        o = sum != 0.f ? make_float4(o.x * al, o.y * al, o.z * al, o.w * al) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
-            for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(&y[u][e]) = __ldcg(reinterpret_cast<const float4*>(x + e));
-          } else {
-            *reinterpret_cast<float2*>(&y[u][0]) = __ldcg(reinterpret_cast<const float2*>(x));
+      for (int u = 0; u < U; ++u)
+        if (ml[u].y != 0.f) {
+          const float w = ex2(ml[u].x - now);
+          if (w != 0.f) {
+            sum = fmaf(w, ml[u].y, sum);
+            o.x = fmaf(w, y[u].x, o.x);
+            o.y = fmaf(w, y[u].y, o.y);
+            o.z = fmaf(w, y[u].z, o.z);
+            o.w = fmaf(w, y[u].w, o.w);
           }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float w = __shfl_sync(0xffffffffu, wt, (k + u) & 31);
-          if (k + u < m && w != 0.f)                 // what an empty range left is not used
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(w, y[u][e], o[e]);
-        }
-      }
     }
-    sum = warp_sum(sum);
   }
   if constexpr (W > 1) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
-    if (lane == 0) s_o[warp][DIM] = sum;
+    s_o[tid] = o;
+    s_ml[tid] = make_float2(top, sum);
     __syncthreads();
-    if (!mine || part) return;
+    if (part) return;
+    float2 ml[W];
+    float w[W];
+    top = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = (s_o[warp][e * 32 + lane] + s_o[warp + 1][e * 32 + lane]) + (s_o[warp + 2][e * 32 + lane] + s_o[warp + 3][e * 32 + lane]);
-    sum = (s_o[warp][DIM] + s_o[warp + 1][DIM]) + (s_o[warp + 2][DIM] + s_o[warp + 3][DIM]);
+    for (int i = 0; i < W; ++i) {
+      ml[i] = s_ml[i * V + tid];
+      if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);
+    }
+    float4 y[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      w[i] = ml[i].y != 0.f ? ex2(ml[i].x - top) : 0.f;
+      ml[i].y = w[i] != 0.f ? ml[i].y * w[i] : 0.f;
+      const float4 z = s_o[i * V + tid];
+      y[i] = w[i] != 0.f ? make_float4(z.x * w[i], z.y * w[i], z.z * w[i], z.w * w[i]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    sum = (ml[0].y + ml[1].y) + (ml[2].y + ml[3].y);
+    o = make_float4((y[0].x + y[1].x) + (y[2].x + y[3].x), (y[0].y + y[1].y) + (y[2].y + y[3].y), (y[0].z + y[1].z) + (y[2].z + y[3].z),
+                    (y[0].w + y[1].w) + (y[2].w + y[3].w));
   }
   if (!mine) return;
   const float inv = sum > 0.f || sum != sum ? __frcp_rn(sum) : 0.f;
-  uint32_t r[E / 2];
-#pragma unroll
-  for (int e = 0; e < E; e += 2) r[e / 2] = pack2<BF16>(o[e] * inv, o[e + 1] * inv);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (long long)(row0 + node) * a.out_stride + qh * DIM) + lane * (E / 2);
-  if constexpr (E == 8)
-    *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
-  else if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(r[0], r[1]);
-  else
-    *dst = r[0];
-  if (lane == 0 && a.lse) a.lse[(long long)(row0 + node) * Hq + qh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  uint16_t* dst = static_cast<uint16_t*>(a.out) + (long long)(s0.x + node) * a.out_stride + (h * a.G + g) * DIM + 4 * cg;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+  if (cg == 0 && a.lse)
+    a.lse[(long long)(s0.x + node) * (a.Hkv * a.G) + h * a.G + g] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
 // --------------------------------------------------------------------- host --
@@ -1066,15 +1119,18 @@ int ta_check(const char* me, const qhl_kv_pages* kv, int Hq, int n_rows, int n_b
 }
 
 template <int DIM, bool BF16>
-cudaError_t ta_launch(const TaArgs& a, int Hq, cudaStream_t s) {
+cudaError_t ta_launch(const TaArgs& a, cudaStream_t s) {
   // each kernel waits for the one before it on the stream before it reads anything
   cudaError_t e = cudaSuccess;
   if (a.n_batch > kTaOwnPlan) e = launch_ex(tree_plan_kernel<DIM>, dim3(1), dim3(512), 0, s, true, a);
   if (e == cudaSuccess) e = launch_ex(tree_attn_kernel<DIM, BF16>, dim3(a.grid), dim3(kTaThreads), TaShape<DIM>::SMEM, s, true, a);
   if (e != cudaSuccess) return e;
-  const long long vectors = (long long)Hq * a.max_nodes * a.n_batch;
-  if (vectors <= kJoinFew) return launch_ex(tree_join_kernel<DIM, BF16, 4>, dim3((unsigned)((vectors + 1) / 2)), dim3(256), 0, s, true, a);
-  return launch_ex(tree_join_kernel<DIM, BF16, 1>, dim3((unsigned)((vectors + 7) / 8)), dim3(256), 0, s, true, a);
+  const int nm = (a.max_nodes * a.G + kTaRows - 1) / kTaRows;
+  const long long values = (long long)a.slot_rows * (DIM / 4) * nm * a.Hkv * a.n_batch;
+  const int v = a.slot_rows * (DIM / 4);
+  const dim3 heads(0, a.Hkv * nm, a.n_batch);
+  if (values <= kJoinFew) return launch_ex(tree_join_kernel<DIM, BF16, 4>, dim3((v + 63) / 64, heads.y, heads.z), dim3(256), 0, s, true, a);
+  return launch_ex(tree_join_kernel<DIM, BF16, 1>, dim3((v + 255) / 256, heads.y, heads.z), dim3(256), 0, s, true, a);
 }
 
 }  // namespace
@@ -1169,11 +1225,11 @@ int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_r
   a.po = reinterpret_cast<float*>(ws + l.po);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dim == 256)
-    e = bf16 ? ta_launch<256, true>(a, n_q_heads, s) : ta_launch<256, false>(a, n_q_heads, s);
+    e = bf16 ? ta_launch<256, true>(a, s) : ta_launch<256, false>(a, s);
   else if (dim == 128)
-    e = bf16 ? ta_launch<128, true>(a, n_q_heads, s) : ta_launch<128, false>(a, n_q_heads, s);
+    e = bf16 ? ta_launch<128, true>(a, s) : ta_launch<128, false>(a, s);
   else
-    e = bf16 ? ta_launch<64, true>(a, n_q_heads, s) : ta_launch<64, false>(a, n_q_heads, s);
+    e = bf16 ? ta_launch<64, true>(a, s) : ta_launch<64, false>(a, s);
   return e == cudaSuccess ? 0 : verify_cuda_err(me, e);
 }
 
