@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeArgs a) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       raw[u][j] = typename Pack<SRC>::V{};
-      if (on && vec < nvec) raw[u][j] = __ldcs(reinterpret_cast<const typename Pack<SRC>::V*>(yr + off + 128 * j) + lane);
+      if (on && vec < nvec) raw[u][j] = __ldg(reinterpret_cast<const typename Pack<SRC>::V*>(yr + off + 128 * j) + lane);
     }
   }
 
