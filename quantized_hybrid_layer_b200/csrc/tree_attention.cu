@@ -6,30 +6,37 @@
 //     S = Q K^T (f32 in tensor memory), p = 2^(c S - c m) with c = scale / ln 2,
 //     O += p V (f32 in tensor memory), l += sum p.
 // m is raised only when a tile's maximum exceeds it by more than 2^8 in p (the
-// result does not depend on m; p stays below 2^8, far inside f16's range), so O
-// is seldom rescaled.  p is rounded to the cache's type for the product; l adds
-// the unrounded p.
+// result does not depend on m), so O is seldom rescaled.  p is rounded to the
+// cache's type for the product, half a step each; l adds the unrounded p.  For f16
+// p is 2^6 larger, 2^14 at most, so that the weights of a long tail are not lost in
+// f16's subnormal numbers.
 //
-// What bounds it: for few query rows the bytes of K and V (one byte of cache
-// feeds 2 query rows x 2 operations per element; a tile of 128 rows needs about
-// half the tensor core's rate at HBM's), for many the products.  Both products
-// run on tcgen05 with M = 128 query rows: all tokens x query heads of one KV
-// head, so a cache row is read once for all of them (a tree with more rows takes
-// several M tiles, whose CTAs read the same tiles at the same time, from L2).
-// A tile of 64 keys x 256 dimensions (128 x 128, 128 x 64) is one 32 KB slot of
-// a ring filled by TMA; p stays in tensor memory, over the S it came from, as
-// the A operand of the second product.
+// What bounds it: for few query rows the bytes of K and V, for many the products.
+// Both products run on tcgen05 with M = 128 query rows: all tokens x query heads of
+// one KV head, so a cache row is read once for all of them; a tree with more rows
+// takes several M tiles, whose CTAs walk the same tiles side by side.  A tile of 64
+// keys x 256 dimensions (128 x 128, 128 x 64) is one 32 KB (16 KB) slot of a 192 KB
+// ring filled by TMA.  Q lies in tensor memory, which frees 64 KB of shared memory
+// for that ring (four slots instead of six: 214 us instead of 189 us for 4 trees of
+// 16 tokens over 65536 rows), and so does p, over the S it came from, as the A
+// operand of the second product.
 //
-// Work split: an item is (tree, KV head, M tile, range of key tiles).  A small
-// planning kernel picks the tiles per item so that the items fill the SMs in
-// few even waves; items of a split range leave (O, m, l) in the workspace and a
-// third kernel joins them in the order of the ranges.  Lengths are read on the
-// device, so one captured graph serves every length.
+// Measured (B200; 6543 GB/s and 1624 TFLOP/s are the measured peaks): 16 tokens of
+// 24 heads over 262001 rows 188 us, 5.7 TB/s; 24 trees of 12 tokens over 16384 rows
+// at 128 dimensions 254 us, 6.4 TB/s; 64 tokens over 4 x 65536 rows 385 us, 1.07
+// PFLOP/s, where the power cap holds the clock at 1.5 to 1.65 GHz and a tile of 64
+// keys takes about 1700 cycles (S: 16 MMAs of N = 64 that cost as much as N = 128
+// would; a second S of 128 columns does not fit beside O and Q).
+//
+// Work split: the CTAs take equal runs of key tiles (see "planning"), from lengths
+// that they read on the device, so one captured graph serves every length.  What is
+// split leaves (O, m, l) in the workspace and a second kernel joins it in the order
+// of the runs, so results do not depend on timing.
 //
 // Roles of a CTA (one per SM): warps 0-7 softmax (warp w: the 32 rows of lane
 // quarter w % 4 and half w / 4 of the keys; O's columns are halved the same way),
-// warp 8 TMA, warp 9 one MMA issuer, warps 10-11 ancestor masks and the tiles
-// that need care.  Rows of V that nobody may see (beyond the sequence, beyond
+// warp 8 TMA, warp 9 issues S, warp 10 issues O, warp 11 ancestor masks and the
+// tiles that need care.  Rows of V that nobody may see (beyond the sequence, beyond
 // the tree, in pages of garbage) are zeroed in shared memory, since 0 * NaN is
 // NaN; a drafted V row's infinities and NaN are taken out the same way and put
 // back, at the end, into the rows of the tokens that see them.
@@ -147,7 +154,7 @@ QHL_DEV TaSeq ta_seq(const TaArgs& a, int b) {
     s.seq = 0;
   } else {
     s.ctx = a.len[s.seq];
-    if (s.ctx < 0 || s.ctx > ((long long)a.max_pages << a.page_shift)) {
+    if (s.ctx < 0 || s.ctx > kTaMostUnits || s.ctx > ((long long)a.max_pages << a.page_shift)) {
       atomicOr(a.err, ERR_BAD_INDEX);
       s.ctx = 0;
     }
@@ -424,6 +431,7 @@ template <int DIM, bool BF16>
 __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_constant__ TaArgs a) {
   using Sh = TaShape<DIM>;
   constexpr int KT = Sh::KT, CH = Sh::CH, NS = Sh::NS, HK = KT / 2;
+  constexpr float kUp = BF16 ? 0.f : 6.f;            // p is 2^kUp larger than its softmax numerator
   static_assert(NS % 2 == 0, "K has the even slots, V the odd ones");
   extern __shared__ uint8_t smem_raw[];
   __shared__ TaBars bars;
@@ -796,7 +804,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
               }
             }
           }
-          const float ms = m == -INFINITY ? 0.f : m * c;
+          const float ms = m == -INFINITY ? 0.f : m * c - kUp;
           const float2 c2 = make_float2(c, c), ms2 = make_float2(-ms, -ms);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -886,7 +894,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
           }
         }
         if (valid && hf == 0) {
-          const float mc = m == -INFINITY ? -INFINITY : m * c;
+          const float mc = m == -INFINITY ? -INFINITY : m * c - kUp;
           if (!whole)
             a.pml[slot] = make_float2(mc, l);
           else if (a.lse)

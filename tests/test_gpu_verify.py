@@ -440,6 +440,45 @@ def test_attention_ragged_batch(q, dim, page, dtype):
     check_attention(q, Trees(ctx, parents, 8, 2, dim, page, DTYPES[dtype], seed=1, extra_rows=3))
 
 
+@pytest.mark.parametrize("kv_heads,group,nodes,ctx", [
+    (3, 2, [4, 4], [1200, 700]),                         # heads that share a run
+    (7, 1, [3], [2000]),
+    (16, 3, [2, 5], [900, 30]),                          # more heads than a group takes
+    (2, 8, [40, 37, 40], [500, 900, 0]),                 # trees of three M tiles: a CTA for each
+    (2, 8, [64] + [1] * 30, [300] + [400] * 30),         # sizes too different for that: M tiles by themselves
+    (1, 128, [5, 3], [1500, 100]),
+    (1, 4, [128, 128], [3000, 5]),
+])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_attention_groups_of_heads_and_tiles(q, kv_heads, group, nodes, ctx, dim):
+    g = gen(sum(nodes))
+    check_attention(q, Trees(ctx, [random_tree(n, g) for n in nodes], kv_heads * group, kv_heads, dim, 16, torch.float16, seed=len(nodes)))
+
+
+def test_attention_infinities_in_a_tree_of_several_tiles_and_parts(q):
+    """The same as above for a tree whose rows and keys are spread over many CTAs."""
+    n, D = 100, 256
+    tree = [i - 2 if i > 1 else -1 for i in range(n)]    # two chains: odd tokens do not see even ones
+    t = Trees([1500], [tree], 4, 2, D, 64, torch.bfloat16, seed=4)
+    clean, clean_lse = run_attention(q, t)
+    t.v_new[10, 0, 7], t.v_new[70, 1, 200] = float("inf"), float("nan")
+    out, lse = run_attention(q, t)
+    assert torch.equal(out[1::2], clean[1::2]) and torch.equal(lse, clean_lse)
+    assert torch.equal(out[:10], clean[:10])
+    assert bool((out[10::2, :2, 7] == float("inf")).all()) and bool(out[70::2, 2:, 200].isnan().all())
+    same = torch.ones(n, 4, D, dtype=torch.bool)
+    same[10::2, :2, 7], same[70::2, 2:, 200] = False, False
+    assert torch.equal(out[same], clean[same])
+    q.qhl_sync()
+
+
+def test_attention_more_trees_than_a_cta_plans_for_itself(q):
+    g = gen(9)
+    ctx = [2500] + torch.randint(0, 40, (270,), generator=g).tolist() + [1100, 0]
+    trees = [random_tree(6, g)] + [[-1]] * 270 + [random_tree(30, g), []]
+    check_attention(q, Trees(ctx, trees, 8, 1, 64, 32, torch.bfloat16, seed=3))
+
+
 def test_attention_many_sequences(q):
     g = gen(6)
     ctx = torch.randint(0, 90, (300,), generator=g).tolist()
@@ -689,4 +728,82 @@ def test_a_verify_step_with_all_operators(q):
     assert kv.lens.tolist()[:3] == [len(history[s]) for s in range(3)]
     q.qhl_pages_free(kv, i32([0, 1, 2]), i32([0, 0, 0]))
     assert kv.refs.tolist() == [0] * n_pages
+    q.qhl_sync()
+
+
+def test_a_verify_step_captured_in_a_graph(q):
+    """Every operator of a step in one graph, with scratch from the allocator, replayed with other inputs; and on a
+    stream of its own."""
+    Hq, H, D, P, L, n = 4, 2, 64, 16, 2, 5
+    dt = torch.float16
+    g = gen(21)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    width = 2 * Hq * D + 2 * H * D
+    Hk, Hv = 2, 2
+
+    def fresh(seed):
+        g = gen(seed)
+        r = lambda *s: torch.randn(*s, generator=g)   # noqa: E731
+        table = torch.full((3, 5), -1, dtype=torch.int32)
+        table[0, :3], table[1, :2] = torch.tensor([4, 1, 7]), torch.tensor([0, 6])
+        refs = torch.zeros(14, dtype=torch.int32)
+        refs[[4, 1, 7, 0, 6]] = 1
+        k = torch.full((L, 14, H, P, D), float("nan")).to(dt)
+        v = k.clone()
+        for p in (4, 1, 7, 0, 6):
+            k[:, p], v[:, p] = r(L, H, P, D).to(dt), r(L, H, P, D).to(dt)
+        dn = r(n, 2 * Hk * 128 + Hv * 128 + 2 * Hv)
+        return dict(k=k, v=v, table=table, lens=torch.tensor([35 + seed % 5, 30, 0], dtype=torch.int32), held=torch.tensor([3, 2, 0], dtype=torch.int32),
+                    refs=refs, at=torch.tensor([35 + seed % 5, 30], dtype=torch.int32), y=r(L, n, width), dn=dn, states=0.1 * r(2, Hv, 128, 128))
+
+    seqs, starts, parent = i32([2, 1]), i32([0, 3, 5]), i32([-1, 0, 0, -1, 0])
+    path, acc = i32([[0, 2], [0, 1]]), i32([2, 2])
+
+    def make(d):
+        kv = q.KvPages(d["k"], d["v"], d["table"], d["lens"], d["held"], d["refs"])
+        o = dict(status=i32([9, 9]), st=i32([9]), qq=torch.zeros(L, n, Hq, D, dtype=dt, device="cuda"), kn=torch.zeros(L, n, H, D, dtype=dt, device="cuda"),
+                 vn=torch.zeros(L, n, H, D, dtype=dt, device="cuda"), out=torch.zeros(L, n, Hq, D, dtype=dt, device="cuda"),
+                 lse=torch.zeros(L, n, Hq, device="cuda"), snaps=torch.zeros(n, Hv, 128, 128, device="cuda"), o=torch.zeros(n, Hv * 128, device="cuda"),
+                 pos=i32([0] * n), one=torch.ones(D, device="cuda"), zero=i32([0, 1]), src=i32([0]), dst=i32([2]), add=i32([3, 2]), kv=kv)
+        return o
+
+    def step(d, o, stream=None):
+        q.qhl_pages_free(o["kv"], o["dst"], o["st"], stream=stream)
+        q.qhl_pages_fork(o["kv"], o["src"], o["dst"], o["st"], stream=stream)
+        q.qhl_pages_extend(o["kv"], seqs, o["add"], o["status"], stream=stream)
+        for layer in range(L):
+            q.qhl_qk_norm_rope(Hq, H, D, D, 1e4, 1e-6, d["y"][layer], o["pos"], o["one"], o["one"], o["qq"][layer], o["kn"][layer], o["vn"][layer], stream=stream)
+            q.qhl_tree_attention(o["kv"], layer, seqs, starts, parent, 3, o["qq"][layer], o["kn"][layer], o["vn"][layer], o["out"][layer],
+                                 lse=o["lse"][layer], stream=stream)
+        q.qhl_deltanet_tree(Hk, Hv, d["dn"], starts, parent, 3, d["states"], o["zero"], o["snaps"], o["o"], stream=stream)
+        q.qhl_pages_commit(o["kv"], seqs, starts, path, acc, d["at"], o["kn"], o["vn"], o["status"], stream=stream)
+
+    def results(d, o):
+        torch.cuda.synchronize()
+        return [x.clone() for x in (d["table"], d["lens"], d["held"], d["refs"], o["status"], o["out"], o["lse"], o["snaps"], o["o"])] + [
+            d["k"].nan_to_num(7.0), d["v"].nan_to_num(7.0)]
+
+    def eager(seed, stream=None):
+        d = {k: x.cuda() for k, x in fresh(seed).items()}
+        o = make(d)
+        torch.cuda.synchronize()
+        step(d, o, stream=stream)
+        return results(d, o)
+
+    want = [eager(s) for s in (1, 2)]
+    for s, w in zip((1, 2), want):
+        assert w[4].tolist() == [0, 0]
+        side = torch.cuda.Stream()
+        for stream in (side, side.cuda_stream):
+            assert all(torch.equal(a, b) for a, b in zip(eager(s, stream), w))
+    d = {k: x.cuda() for k, x in fresh(1).items()}
+    o = make(d)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(d, o)
+    for s, w in ((1, want[0]), (2, want[1]), (1, want[0])):
+        for k, x in fresh(s).items():
+            d[k].copy_(x)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(results(d, o), w))
     q.qhl_sync()
