@@ -485,9 +485,12 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
 
   if (warp == 8) {
     // ---------------------------------------------------------------- TMA --
-    // A copy per (box of rows, chunk) where a box is less than a tile, so that the
-    // chunks of all boxes are KT rows apart in the slot; the lanes issue them
-    // together.
+    // Where a page is less than a tile, a tile takes several copies, which the lanes
+    // issue together.  K: one per (page, chunk), so that the chunks of all pages are
+    // KT rows apart in the slot (the product's N runs over the rows of all pages).
+    // V: one per page, whose chunks follow one another (the product takes 16 rows at
+    // a time, which lie in one page); a small copy costs as much as a large one, and
+    // with pages of 16 rows the copies are what bounds a tile.
     uint32_t r = 0;
     const int pchunks = a.box == KT ? 1 : CH, dchunks = a.dbox == KT ? 1 : CH;
     const int pbox = lane / pchunks, pchunk = lane % pchunks, boxes_per_tile = KT >> a.box_shift;
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
       for (int tile = w.t0; ok && tile < w.t1; ++tile) {
         const bool draft = tile >= w.nct;
         const int b0 = tile * boxes_per_tile;
-        int nb = 1, pg = 0, rr = w.s.row0 + (tile - w.nct) * KT;
+        int nb = 1;
         if (!draft) {
           nb = min(boxes_per_tile, box_end - b0);
           if (b0 - ids_at >= 32) {                   // 32 is a multiple of a tile's boxes
@@ -519,13 +522,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
             ids_at += 32;
             ids_next = page_of(ids_at + 32 + lane);
           }
-          pg = __shfl_sync(0xffffffffu, ids, (b0 - ids_at + pbox) & 31);
-          rr = (b0 + pbox) << a.box_shift & ((1 << a.page_shift) - 1);
         }
-        const int copies = draft ? dchunks : nb * pchunks;
         const uint32_t bytes = (uint32_t)(draft ? a.dbox : nb << a.box_shift) * DIM * 2;
-        const int c = draft ? lane : pchunk;
-        const uint32_t off = (draft ? 0u : (uint32_t)(pbox << a.box_shift) * 128u) + (uint32_t)c * (KT * 128);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const uint32_t s = r % NS, ph = r / NS & 1;
@@ -534,8 +532,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(bar(bars.full[s]), bytes);
           __syncwarp();
-          if (lane < copies)
-            tma_load_5d(ring + s * Sh::SLOT + off, draft ? (kv ? &a.vn : &a.kn) : (kv ? &a.v : &a.k), bar(bars.full[s]), rr, c, w.h, pg);
+          const uint32_t dst = ring + s * Sh::SLOT;
+          if (draft) {
+            if (lane < dchunks) tma_load_5d(dst + lane * (KT * 128), kv ? &a.vn : &a.kn, bar(bars.full[s]), w.s.row0 + (tile - w.nct) * KT, lane, w.h, 0);
+          } else {
+            const int box = kv ? lane : pbox, c = kv ? 0 : pchunk;
+            const int pg = __shfl_sync(0xffffffffu, ids, (b0 - ids_at + box) & 31);
+            const int rr = (b0 + box) << a.box_shift & ((1 << a.page_shift) - 1);
+            const uint32_t off = kv ? (uint32_t)(box << a.box_shift) * (DIM * 2) : (uint32_t)(box << a.box_shift) * 128u + (uint32_t)c * (KT * 128);
+            if (box < nb) tma_load_5d(dst + off, kv ? &a.v : &a.k, bar(bars.full[s]), rr, c, w.h, pg);
+          }
         }
       }
     }
@@ -594,10 +600,14 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
         tc_fence_after();
         if (elect_one()) {
           const uint32_t p = tmem + Sh::S0 + b * KT;
-          const uint64_t vd = smem_desc_sw128(ring + slot * Sh::SLOT, KT * 128);
+          // chunks are a page's (or a tile's) rows apart, pages follow one another
+          const int shift = tile >= nct ? (KT == 64 ? 6 : 7) : a.box_shift, rows = 1 << shift;
+          const uint64_t vd = smem_desc_sw128(ring + slot * Sh::SLOT, rows * 128);
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            if (16 * k < keys) mma_f16_ts(tmem, p + k * 8, vd + (uint64_t)(k * 2048 >> 4), id, tile != t0 || k);
+          for (int k = 0; k < KT / 16; ++k) {
+            const int off = (16 * k >> shift << shift) * (DIM * 2) + (16 * k & (rows - 1)) * 128;
+            if (16 * k < keys) mma_f16_ts(tmem, p + k * 8, vd + (uint64_t)(off >> 4), id, tile != t0 || k);
+          }
           tc_commit(&bars.pv_done[b]);
           tc_commit(&bars.empty[slot]);
         }
@@ -676,7 +686,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
         const int end = (keys + 15) & ~15, begin = draft ? 0 : keys;
 #pragma unroll 1
         for (int ch = 0; ch < CH; ++ch) {
-          uint4* p = reinterpret_cast<uint4*>(base + ch * (KT * 128));
+          // row 0 of the chunk, as if the rows of the last page (or the tile) began at 0
+          const int shift = draft ? (KT == 64 ? 6 : 7) : a.box_shift, page0 = begin >> shift << shift;
+          uint4* p = reinterpret_cast<uint4*>(base + page0 * (DIM * 2) + (ch << shift) * 128 - page0 * 128);
 #pragma unroll 4
           for (int u = begin * 8 + lane; u < keys * 8; u += 32) {
             uint4 x = p[u];
@@ -1195,10 +1207,10 @@ int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_r
   const uint16_t* kb = static_cast<const uint16_t*>(kv->k_dev) + (long long)layer * kv->stride_layer;
   const uint16_t* vb = static_cast<const uint16_t*>(kv->v_dev) + (long long)layer * kv->stride_layer;
   const long long pd[4] = {P, CH, kv->kv_heads, kv->n_pages}, ps[4] = {kv->stride_row, 64, kv->stride_head, kv->stride_page};
-  const int pb[4] = {a.box, a.box == KT ? CH : 1, 1, 1};
+  const int kb4[4] = {a.box, a.box == KT ? CH : 1, 1, 1}, vb4[4] = {a.box, CH, 1, 1};
   const long long nd[4] = {n_rows, CH, kv->kv_heads, 1}, ns[4] = {new_stride, 64, dim, 64};
   const int nb[4] = {a.dbox, a.dbox == KT ? CH : 1, 1, 1};
-  const bool fine = encode(&a.k, bf16, kb, pd, ps, pb) && encode(&a.v, bf16, vb, pd, ps, pb) && encode(&a.kn, bf16, k_new_dev, nd, ns, nb) &&
+  const bool fine = encode(&a.k, bf16, kb, pd, ps, kb4) && encode(&a.v, bf16, vb, pd, ps, vb4) && encode(&a.kn, bf16, k_new_dev, nd, ns, nb) &&
               encode(&a.vn, bf16, v_new_dev, nd, ns, nb);
   if (!fine) return verify_err(me, STAGE_E_UNSUPPORTED, "the driver refused a tensor map for these strides");
   auto log2i = [](int x) { int n = 0; while (1 << n < x) ++n; return n; };
