@@ -19,10 +19,14 @@
 // o = S . q of a token and the S . k of the next (both of the state between them)
 // are reduced together: each of the first three butterfly steps halves the number
 // of values a lane carries, so eight sums take 9 shuffles and 5 steps of latency
-// instead of 40 and 10 (16 tokens of 48 heads: 20.0 us before, with one reduction
-// after the other).  A sum's tree of additions is that of the plain butterfly
+// instead of 40 and 10.  A sum's tree of additions is that of the plain butterfly
 // (offsets 16, 8, 4, 2, 1), so a path's results have the same bits as the chained
 // steps of qhl_deltanet_step.
+//
+// The inputs of 16 tokens at a time come by asynchronous copies, a block ahead (as
+// loads in turn they took 3.3 us a block).  Measured: one tree of 16 tokens and 48
+// heads 15.4 us for 53.5 MB (3.5 TB/s: the chain of tokens), eight ragged trees,
+// 426 MB, 79.7 us (5.3 TB/s; a plain fill of 400 MB reaches 7.2 TB/s).
 //
 // No early start of the kernel behind this one (20.0 us against 24.3): its waiting
 // CTAs, spread unevenly, would take this kernel's places.
@@ -88,9 +92,10 @@ QHL_DEV int tree_by_size(const int* q_start, int n_batch, int rank) {
 }
 
 // One block of tokens' inputs, brought in by asynchronous copies.
+template <int ROWS>
 struct DtStage {
   float4 q[kDtBlock][32], k[kDtBlock][32];
-  float v[kDtBlock][32], b[kDtBlock], a[kDtBlock];
+  float v[kDtBlock][ROWS], b[kDtBlock], a[kDtBlock];
 };
 
 QHL_DEV void copy_async16(void* dst, const void* src) {
@@ -101,17 +106,18 @@ QHL_DEV void copy_async4(void* dst, const void* src) {
 }
 QHL_DEV void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <int R, int PER_SM>
-__global__ void __launch_bounds__(1024 / R, PER_SM) dn_tree_kernel(const DnTreeArgs a) {
-  constexpr int THREADS = 1024 / R, WARPS = THREADS / 32, STEP = 16 / R;   // STEP: lanes per total
+// R value rows per warp, ROWS per CTA.
+template <int R, int ROWS, int PER_SM>
+__global__ void __launch_bounds__(ROWS / R * 32, PER_SM) dn_tree_kernel(const DnTreeArgs a) {
+  constexpr int WARPS = ROWS / R, THREADS = WARPS * 32, PARTS = kDnDim / ROWS, STEP = 16 / R;   // STEP: lanes per total
   constexpr int kStay = -4;   // the node's parent is the last living node: its state is in S
-  __shared__ __align__(16) DtStage stage[2];
+  __shared__ __align__(16) DtStage<ROWS> stage[2];
   __shared__ int sj[kMaxNodes];              // parents, then by doubling -1 (living) or -2 (padded)
   __shared__ short s_node[kMaxNodes + 1];    // the living nodes in order
   __shared__ short s_from[kMaxNodes + 1];    // where each starts: kStay, -1 (the cached state) or a node
   __shared__ unsigned s_alive[kMaxNodes / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x >> 2, part = blockIdx.x & 3, row0 = part * 32 + warp * R;
+  const int h = blockIdx.x / PARTS, part = blockIdx.x % PARTS, row0 = part * ROWS + warp * R;
   const int g = h / (a.Hv / a.Hk);
   const int off_k = a.Hk * kDnDim, off_v = 2 * off_k, off_b = off_v + a.Hv * kDnDim, off_a = off_b + a.Hv;
   const size_t state_elems = (size_t)a.Hv * kDnDim * kDnDim;
@@ -124,7 +130,7 @@ __global__ void __launch_bounds__(1024 / R, PER_SM) dn_tree_kernel(const DnTreeA
   tree_rows(a.q_start, tree, a.n_rows, a.max_nodes, first, n, a.err);
   if (n == 0) return;
 
-  auto stage_in = [&](DtStage& s, int base) {
+  auto stage_in = [&](DtStage<ROWS>& s, int base) {
     const int m = min(kDtBlock, n - base);
     const float* y = a.y + (size_t)(first + base) * a.y_stride;
     for (int i = tid; i < m * 64; i += THREADS) {
@@ -132,8 +138,8 @@ __global__ void __launch_bounds__(1024 / R, PER_SM) dn_tree_kernel(const DnTreeA
       const bool is_k = i & 32;
       copy_async16(is_k ? &s.k[t][c] : &s.q[t][c], y + (size_t)t * a.y_stride + (is_k ? off_k : 0) + g * kDnDim + 4 * c);
     }
-    for (int i = tid; i < m * 32; i += THREADS)
-      copy_async4(&s.v[i >> 5][i & 31], y + (size_t)(i >> 5) * a.y_stride + off_v + h * kDnDim + part * 32 + (i & 31));
+    for (int i = tid; i < m * ROWS; i += THREADS)
+      copy_async4(&s.v[i / ROWS][i % ROWS], y + (size_t)(i / ROWS) * a.y_stride + off_v + h * kDnDim + part * ROWS + i % ROWS);
     if (tid < 2 * m) {
       const int t = tid >> 1;
       copy_async4(tid & 1 ? &s.a[t] : &s.b[t], y + (size_t)t * a.y_stride + (tid & 1 ? off_a : off_b) + h);
@@ -201,8 +207,10 @@ __global__ void __launch_bounds__(1024 / R, PER_SM) dn_tree_kernel(const DnTreeA
 #pragma unroll
   for (int w = 0; w < kMaxNodes / 32; ++w) living += __popc(s_alive[w]);
   if (living < n) {                          // padded nodes: their outputs are 0
-    for (int i = tid; i < n * 32; i += THREADS)
-      if (!(s_alive[i >> 10] >> (i >> 5 & 31) & 1)) a.o[(size_t)(first + (i >> 5)) * a.Hv * kDnDim + h * kDnDim + part * 32 + (i & 31)] = 0.f;
+    for (int i = tid; i < n * ROWS; i += THREADS) {
+      const int x = i / ROWS;
+      if (!(s_alive[x >> 5] >> (x & 31) & 1)) a.o[(size_t)(first + x) * a.Hv * kDnDim + h * kDnDim + part * ROWS + i % ROWS] = 0.f;
+    }
   }
   if (tid == 0) {
     s_node[living] = kMaxNodes;              // behind every block
@@ -216,7 +224,7 @@ __global__ void __launch_bounds__(1024 / R, PER_SM) dn_tree_kernel(const DnTreeA
   int at = 0;
   for (int base = 0; base < n; base += kDtBlock) {
     const int m = min(kDtBlock, n - base);
-    DtStage& s = stage[base / kDtBlock & 1];
+    DtStage<ROWS>& s = stage[base / kDtBlock & 1];
     copy_async_wait();
     __syncthreads();
     for (int t = warp; t < m; t += WARPS) {
@@ -309,10 +317,13 @@ extern "C" int qhl_deltanet_tree(int Hk, int Hv, const float* y_dev, int n_rows,
                   state_index_dev, snaps_dev, o_dev, nullptr};
   cudaError_t e = verify_error_word(&a.err);
   if (e != cudaSuccess) return verify_cuda_err(me, e);
-  // Up to two CTAs per SM the registers of three are of no use: 16 tokens of 48 heads
-  // take 16.5 us with all that the kernel wants, 17.6 us with 80; eight such trees
-  // 84.2 us and 78.6 us.
-  auto kernel = (long long)Hv * 4 * n_batch <= 2 * 148 ? dn_tree_kernel<kDtRows, 2> : dn_tree_kernel<kDtRows, 3>;
-  e = launch_ex(kernel, dim3(Hv * 4, n_batch), dim3(1024 / kDtRows), 0, static_cast<cudaStream_t>(stream), true, a);
+  // Few CTAs: 16 rows each, spread more evenly, with all the registers that the
+  // kernel wants (one tree of 16 tokens, 48 heads: 15.4 us, with 32 rows 16.5 us).
+  // Many: 32 rows and registers for three CTAs per SM (eight such trees: 78.6 us,
+  // with two per SM 84.2 us).
+  const bool few = (long long)Hv * 4 * n_batch <= 2 * 148;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  e = few ? launch_ex(dn_tree_kernel<kDtRows, 16, 4>, dim3(Hv * 8, n_batch), dim3(128), 0, s, true, a)
+          : launch_ex(dn_tree_kernel<kDtRows, 32, 3>, dim3(Hv * 4, n_batch), dim3(256), 0, s, true, a);
   return e == cudaSuccess ? 0 : verify_cuda_err(me, e);
 }
