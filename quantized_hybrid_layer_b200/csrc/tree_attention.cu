@@ -990,7 +990,7 @@ __global__ void __launch_bounds__(256, W > 1 ? 3 : 5) tree_join_kernel(const __g
       for (int u = 0; u < U; ++u)
         if (ml[u].y != 0.f) {
           const float w = ex2(ml[u].x - now);
-          if (w != 0.f) {
+          if (w != 0.f || ml[u].y != ml[u].y) {      // a NaN counts whatever its weight
             sum = fmaf(w, ml[u].y, sum);
             o.x = fmaf(w, y[u].x, o.x);
             o.y = fmaf(w, y[u].y, o.y);
@@ -1017,9 +1017,10 @@ __global__ void __launch_bounds__(256, W > 1 ? 3 : 5) tree_join_kernel(const __g
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       w[i] = ml[i].y != 0.f ? ex2(ml[i].x - top) : 0.f;
-      ml[i].y = w[i] != 0.f ? ml[i].y * w[i] : 0.f;
+      const bool use = w[i] != 0.f || ml[i].y != ml[i].y;
+      ml[i].y = use ? ml[i].y * w[i] : 0.f;
       const float4 z = s_o[i * V + tid];
-      y[i] = w[i] != 0.f ? make_float4(z.x * w[i], z.y * w[i], z.z * w[i], z.w * w[i]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      y[i] = use ? make_float4(z.x * w[i], z.y * w[i], z.z * w[i], z.w * w[i]) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     sum = (ml[0].y + ml[1].y) + (ml[2].y + ml[3].y);
     o = make_float4((y[0].x + y[1].x) + (y[2].x + y[3].x), (y[0].y + y[1].y) + (y[2].y + y[3].y), (y[0].z + y[1].z) + (y[2].z + y[3].z),

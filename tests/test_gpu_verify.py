@@ -528,6 +528,18 @@ def test_attention_hidden_infinities_stay_hidden(q, dtype, dim):
     q.qhl_sync()
 
 
+@pytest.mark.parametrize("ctx", [0, 40, 3000])
+def test_attention_a_token_whose_own_key_is_nan(q, ctx):
+    """NaN stays NaN where the parts of a token are joined, also from a part whose scores are all NaN."""
+    t = Trees([ctx], [[-1, -1]], 2, 1, 256, 64, torch.float16, seed=4)
+    clean, clean_lse = run_attention(q, t)
+    t.k_new[1, 0, 9] = float("nan")
+    out, lse = run_attention(q, t)
+    assert torch.equal(out[0], clean[0]) and torch.equal(lse[0], clean_lse[0])
+    assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
+    q.qhl_sync()
+
+
 def test_attention_padded_tokens_over_a_cache_with_infinities(q):
     t = Trees([100], [[-1, -2]], 2, 1, 256, 64, torch.bfloat16, seed=4)
     t.v[0, int(t.table[0, 0]), 0, 5, 7] = float("inf")
