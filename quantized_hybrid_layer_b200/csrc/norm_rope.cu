@@ -6,15 +6,18 @@
 // for the leading R dimensions, with i < R / 2 and a = pos * theta^(-2 i / R):
 //     out_i = z_i cos a - z_{i + R/2} sin a,   out_{i + R/2} = z_{i + R/2} cos a + z_i sin a.
 //
-// Bound by HBM: every element is read and written once.  One warp holds V head
-// vectors of one token in registers (lane l: the four elements 4l.. of each 128,
-// so every load and store is a run of whole sectors); their loads are issued
-// together, and the angles, which all heads of a token share, are formed while
-// they are in flight.  The partner of a rotated element comes from shared
-// memory.  Angles reach pos * 1 = 262144 rad, where an f32 is 2^-6 apart: the
-// product and its reduction to turns are 64-bit (a handful of instructions per
-// warp), and theta^(-2 i / R) is a product of at most seven factors
+// Bound by HBM: every element is read and written once.  A lane holds eight elements,
+// so a warp holds 256 / D head vectors of one token at a time, V times; their loads are issued together, and the angles, which all heads of a
+// token share, are formed while they are in flight.  The partner of a rotated
+// element comes from shared memory.  Angles reach pos * 1 = 262144 rad, where an f32
+// is 2^-6 apart: the product and its reduction to turns are 64-bit (a handful of
+// instructions per warp), and theta^(-2 i / R) is a product of at most seven factors
 // theta^(-2^(j+1) / R), one for each bit j of i, so no table is read.
+//
+// Measured: 8191 tokens of 24 + 4 + 4 heads of 256, f32 to bf16, 71.1 us, 5.7 TB/s
+// (0.87 of the measured copy); of 96 + 8 + 8 heads of 64 59.4 us, 5.9 TB/s; from
+// bf16 rows 4.0 to 4.6 TB/s, bound by the instructions.  One token: 2.4 us of GPU
+// time, a launch.
 #include <algorithm>
 
 #include "launch.h"
@@ -68,34 +71,34 @@ struct Pack<__nv_bfloat16> {
   }
 };
 
-// A warp's task: V consecutive head vectors (q heads, then k, then v) of a row.
-// J groups of 128 dimensions per vector; at D = 64 the upper half-warp idles in
-// the loads of a vector (its lanes hold zeros).
+// A warp's task: V times NP consecutive head vectors (q heads, then k, then v) of a
+// row.  Lane l has a part of vector l / LPV: the four elements 4 (l % LPV) .. of each
+// half of it, so that every load and store of a warp is a run of whole sectors and
+// the partner of an element that is rotated with all of its vector is in the lane.
 template <typename SRC, typename DST, int D, int V>
 __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeArgs a) {
-  constexpr int J = D > 128 ? D / 128 : 1;
-  __shared__ float2 s_turn[8][D / 2];
-  __shared__ __align__(16) float s_vec[8][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nvec = a.hq + 2 * a.hkv, per_row = (nvec + V - 1) / V;
+  constexpr int LPV = D / 8, NP = 32 / LPV;
+  __shared__ __align__(16) float2 s_turn[8][D / 2];
+  __shared__ __align__(16) float s_vec[8][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPV, d0 = lane % LPV * 4;
+  const int nvec = a.hq + 2 * a.hkv, per_row = (nvec + V * NP - 1) / (V * NP);
   const long long task = (long long)blockIdx.x * 8 + warp;
   if (threadIdx.x == 0) pdl_launch();
   if (task >= (long long)a.n_rows * per_row) return;
   pdl_wait();
-  const int row = (int)(task / per_row), v0 = (int)(task % per_row) * V;
-  const bool on = D >= 128 || 4 * lane < D;
+  const int row = (int)(task / per_row), v0 = (int)(task % per_row) * V * NP;
 
-  const SRC* yr = static_cast<const SRC*>(a.y) + (long long)row * a.y_stride;
-  typename Pack<SRC>::V raw[V][J];
+  const SRC* yr = static_cast<const SRC*>(a.y) + (long long)row * a.y_stride + d0;
+  typename Pack<SRC>::V raw[V][2];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    const int vec = v0 + u;
+    const int vec = v0 + u * NP + sub;
     const int off = vec < a.hq ? a.q_off + vec * D
                                : vec < a.hq + a.hkv ? a.k_off + (vec - a.hq) * D : a.v_off + (vec - a.hq - a.hkv) * D;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
+    for (int j = 0; j < 2; ++j) {
       raw[u][j] = typename Pack<SRC>::V{};
-      if (on && vec < nvec) raw[u][j] = __ldg(reinterpret_cast<const typename Pack<SRC>::V*>(yr + off + 128 * j) + lane);
+      if (vec < nvec) raw[u][j] = __ldg(reinterpret_cast<const typename Pack<SRC>::V*>(yr + off + j * (D / 2)));
     }
   }
 
@@ -118,69 +121,76 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeArgs a) {
 
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    const int vec = v0 + u;
-    if (vec >= nvec) return;
+    const int vec = v0 + u * NP + sub;
     const int kind = vec < a.hq ? 0 : vec < a.hq + a.hkv ? 1 : 2;
     const int head = vec - (kind == 0 ? 0 : kind == 1 ? a.hq : a.hq + a.hkv);
-    float x[J][4];
-#pragma unroll
-    for (int j = 0; j < J; ++j) Pack<SRC>::get(raw[u][j], x[j]);
-    if (kind < 2) {
+    float x[2][4];
+    Pack<SRC>::get(raw[u][0], x[0]);
+    Pack<SRC>::get(raw[u][1], x[1]);
+    if (v0 + u * NP < a.hq + a.hkv) {                // some vector of the warp is normalised
       float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < J; ++j)
+      for (int e = 0; e < 8; ++e) ss = __fmaf_rn(x[e >> 2][e & 3], x[e >> 2][e & 3], ss);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ss = __fmaf_rn(x[j][e], x[j][e], ss);
-      ss = warp_sum(ss);
+      for (int o = LPV / 2; o > 0; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
       const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.f / D), a.eps)));
-      const float* gamma = kind == 0 ? a.gq : a.gk;
-      if (on) {
+      if (kind < 2) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const float4 g = __ldg(reinterpret_cast<const float4*>(gamma + 128 * j) + lane);
+        for (int j = 0; j < 2; ++j) {
+          const float4 g = __ldg(reinterpret_cast<const float4*>((kind == 0 ? a.gq : a.gk) + d0 + j * (D / 2)));
           x[j][0] *= r * g.x; x[j][1] *= r * g.y; x[j][2] *= r * g.z; x[j][3] *= r * g.w;
-          if (128 * j < a.rope)
-            reinterpret_cast<float4*>(s_vec[warp] + 128 * j)[lane] = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
         }
       }
-      __syncwarp();
-      // half is a multiple of 4: a lane's four elements lie on one side of it
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int d = 128 * j + 4 * lane;
-        if (on && d < a.rope) {
-          const bool low = d < half;
-          const int i = low ? d : d - half;
-          const float4 o = *reinterpret_cast<const float4*>(s_vec[warp] + (low ? d + half : i));
-          const float p[4] = {o.x, o.y, o.z, o.w};
+      if (a.rope == D) {
+        if (kind < 2) {
+          const float4 t0 = *reinterpret_cast<const float4*>(&s_turn[warp][d0]), t1 = *reinterpret_cast<const float4*>(&s_turn[warp][d0 + 2]);
+          const float cs[4] = {t0.x, t0.z, t1.x, t1.z}, sn[4] = {t0.y, t0.w, t1.y, t1.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 t = s_turn[warp][i + e];
-            x[j][e] = low ? x[j][e] * t.x - p[e] * t.y : x[j][e] * t.x + p[e] * t.y;
+            const float p = x[0][e], o = x[1][e];
+            x[0][e] = p * cs[e] - o * sn[e];
+            x[1][e] = o * cs[e] + p * sn[e];
           }
         }
-      }
-      __syncwarp();
-    }
-    if (on) {
-      DST* dst = static_cast<DST*>(a.out[kind]) + (long long)row * a.out_stride[kind] + head * D;
+      } else if (half) {
+        float* mine = s_vec[warp] + sub * D;
 #pragma unroll
-      for (int j = 0; j < J; ++j) reinterpret_cast<uint2*>(dst + 128 * j)[lane] = Pack<DST>::put(x[j]);
+        for (int j = 0; j < 2; ++j)
+          if (kind < 2 && d0 + j * (D / 2) < a.rope) *reinterpret_cast<float4*>(mine + d0 + j * (D / 2)) = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
+        __syncwarp();
+        // half is a multiple of 4: a lane's four elements lie on one side of it
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int d = d0 + j * (D / 2);
+          if (kind < 2 && d < a.rope) {
+            const bool low = d < half;
+            const int i = low ? d : d - half;
+            const float4 o = *reinterpret_cast<const float4*>(mine + (low ? d + half : i));
+            const float4 t0 = *reinterpret_cast<const float4*>(&s_turn[warp][i]), t1 = *reinterpret_cast<const float4*>(&s_turn[warp][i + 2]);
+            const float p[4] = {o.x, o.y, o.z, o.w}, cs[4] = {t0.x, t0.z, t1.x, t1.z}, sn[4] = {t0.y, t0.w, t1.y, t1.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[j][e] = low ? x[j][e] * cs[e] - p[e] * sn[e] : x[j][e] * cs[e] + p[e] * sn[e];
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (vec < nvec) {
+      DST* dst = static_cast<DST*>(a.out[kind]) + (long long)row * a.out_stride[kind] + head * D + d0;
+      *reinterpret_cast<uint2*>(dst) = Pack<DST>::put(x[0]);
+      *reinterpret_cast<uint2*>(dst + D / 2) = Pack<DST>::put(x[1]);
     }
   }
 }
 
 template <typename SRC, typename DST, int D>
 static cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
-  const int nvec = a.hq + 2 * a.hkv;
-  // Few rows: one vector per warp, over as many SMs as there are; many: four per
-  // warp, so that a warp keeps 4 KB in flight and forms the angles once (8191 rows:
-  // two per warp 73.8 us, four 70.1 us, eight 92.3 us).
-  const bool many = (long long)a.n_rows * nvec >= 148LL * 64 * 4;
-  const long long tasks = (long long)a.n_rows * (many ? (nvec + 3) / 4 : nvec);
-  const unsigned grid = (unsigned)((tasks + 7) / 8);
-  return many ? launch_ex(norm_rope_kernel<SRC, DST, D, 4>, dim3(grid), dim3(256), 0, s, true, a)
-              : launch_ex(norm_rope_kernel<SRC, DST, D, 1>, dim3(grid), dim3(256), 0, s, true, a);
+  // Four loads per lane in flight whatever the number of rows (with one: 88.0 us
+  // instead of 71.1 us for 8191 rows, 6.9 us instead of 6.0 us for 512, the same for
+  // one row).
+  constexpr int V = 4, NP = 256 / D;
+  const long long tasks = (long long)a.n_rows * ((a.hq + 2 * a.hkv + V * NP - 1) / (V * NP));
+  return launch_ex(norm_rope_kernel<SRC, DST, D, V>, dim3((unsigned)((tasks + 7) / 8)), dim3(256), 0, s, true, a);
 }
 
 template <typename SRC, typename DST>
