@@ -7,9 +7,10 @@
 //     out_i = z_i cos a - z_{i + R/2} sin a,   out_{i + R/2} = z_{i + R/2} cos a + z_i sin a.
 //
 // Bound by HBM: every element is read and written once.  A lane holds eight elements,
-// so a warp holds 256 / D head vectors of one token at a time, V times; their loads are issued together, and the angles, which all heads of a
-// token share, are formed while they are in flight.  The partner of a rotated
-// element comes from shared memory.  Angles reach pos * 1 = 262144 rad, where an f32
+// so a warp holds 256 / D head vectors of one token at a time, V times; their loads
+// are issued together, and the angles, which all heads of a token share, are formed
+// while they are in flight.  The partner of a rotated element is in the lane where
+// the whole vector is rotated, and comes from shared memory otherwise.  Angles reach pos * 1 = 262144 rad, where an f32
 // is 2^-6 apart: the product and its reduction to turns are 64-bit (a handful of
 // instructions per warp), and theta^(-2 i / R) is a product of at most seven factors
 // theta^(-2^(j+1) / R), one for each bit j of i, so no table is read.
@@ -185,12 +186,16 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeArgs a) {
 
 template <typename SRC, typename DST, int D>
 static cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
-  // Four loads per lane in flight whatever the number of rows (with one: 88.0 us
-  // instead of 71.1 us for 8191 rows, 6.9 us instead of 6.0 us for 512, the same for
-  // one row).
-  constexpr int V = 4, NP = 256 / D;
-  const long long tasks = (long long)a.n_rows * ((a.hq + 2 * a.hkv + V * NP - 1) / (V * NP));
-  return launch_ex(norm_rope_kernel<SRC, DST, D, V>, dim3((unsigned)((tasks + 7) / 8)), dim3(256), 0, s, true, a);
+  // Few vectors, all in one wave of warps: one pass per warp (one row of 32 heads
+  // 3.2 us a call, 64 rows 3.2 us; with four passes 4.0 and 5.1 us).  Many: four, so
+  // that a warp has four loads per lane in flight and forms the angles once (512 rows
+  // 6.0 us, 8191 rows 71.1 us; with one pass 6.9 and 88.0 us).
+  constexpr int NP = 256 / D;
+  const int nvec = a.hq + 2 * a.hkv, one = (nvec + NP - 1) / NP, four = (nvec + 4 * NP - 1) / (4 * NP);
+  const bool few = (long long)a.n_rows * one <= 148 * 48;
+  const dim3 grid((unsigned)(((long long)a.n_rows * (few ? one : four) + 7) / 8));
+  return few ? launch_ex(norm_rope_kernel<SRC, DST, D, 1>, grid, dim3(256), 0, s, true, a)
+             : launch_ex(norm_rope_kernel<SRC, DST, D, 4>, grid, dim3(256), 0, s, true, a);
 }
 
 template <typename SRC, typename DST>
