@@ -209,28 +209,29 @@ QHL_DEV TaHead ta_head(const TaArgs& a, long long alone, long long together, int
   return h;
 }
 
-QHL_DEV long long warp_total(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
 // The plan of at most 32 trees, by one warp: lane b gets tree b.
 template <int KT>
 QHL_DEV TaHead ta_plan_warp(const TaArgs& a, TaSeq& s) {
   const int lane = threadIdx.x & 31;
   s = TaSeq{};
   if (lane < a.n_batch) s = ta_seq<KT>(a, lane);
-  const long long together = (long long)a.Hkv * ta_units(s);
-  const TaHead h = ta_head(a, warp_total(together * s.nm), warp_total(together), __reduce_max_sync(0xffffffffu, s.nm));
-  const int mine = h.units ? ta_segments(s, h, a.Hkv) * ta_units(s) : 0;
-  int inc = mine;
+  // 32 of the most still fit 32 bits; a tree beyond it counts as too many units
+  constexpr long long kMost = kTaMostUnits / 32;
+  const long long mine64 = (long long)a.Hkv * ta_units(s) * s.nm;
+  const bool fits = __all_sync(0xffffffffu, mine64 <= kMost);
+  const int alone = __reduce_add_sync(0xffffffffu, (int)min(mine64, kMost));
+  const int together = __reduce_add_sync(0xffffffffu, (int)min((long long)a.Hkv * ta_units(s), kMost));
+  const TaHead h = ta_head(a, fits ? alone : 2 * kTaMostUnits * a.Hkv, fits ? together : 2 * kTaMostUnits * a.Hkv, __reduce_max_sync(0xffffffffu, s.nm));
+  if (a.n_batch > 1) {
+    const int mine = h.units ? ta_segments(s, h, a.Hkv) * ta_units(s) : 0;
+    int inc = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    s.base = inc - mine;
   }
-  s.base = inc - mine;
   return h;
 }
 
@@ -313,7 +314,9 @@ struct TaOwnPlan {
   TaSeq seq[kTaOwnPlan];
   long long scratch[kTaThreads / 32];
   TaHead head;
-  int first_b;       // the tree that the CTA's run starts in
+  // the CTA's run: units u .. end - 1, from unit x of segment seg of tree b on; its
+  // head and M tile within the group; segments of a tree per M tile of its own
+  int u, end, b, seg, x, hd, mt, head_groups;
 };
 
 // What the roles know of an item.
@@ -323,24 +326,33 @@ struct TaItem {
   QHL_DEV bool whole() const { return t0 == 0 && t1 == s.tiles; }
 };
 
+// The CTA's run, but for where it starts; one thread calls it.
+QHL_DEV void ta_set_run(const TaArgs& a, const TaHead& h, TaOwnPlan& p) {
+  const int per = h.heads * h.tiles, run = (int)blockIdx.x / per, j = (int)blockIdx.x - run * per;
+  p.head = h;
+  p.hd = j / h.tiles;
+  p.mt = j - p.hd * h.tiles;
+  p.head_groups = a.Hkv / h.heads;
+  p.u = run < h.runs ? ta_run_start(h, run) : 0;
+  p.end = run < h.runs ? ta_run_start(h, run + 1) : 0;
+  p.b = p.seg = p.x = 0;
+}
+// Where it starts, from the tree that has its first unit.
+QHL_DEV void ta_set_start(TaOwnPlan& p, int b, const TaSeq& s, int u) {
+  const int units = ta_units(s), at = u - s.base;
+  p.b = b;
+  p.seg = at / units;
+  p.x = at - p.seg * units;
+}
+
 // The items of a CTA, in order.
 template <int DIM>
 struct TaCursor {
-  int u, end;
-  int b, head, mt;             // the tree; the CTA's head and M tile within its group
+  int u, end, b, seg, x;
 
-  QHL_DEV TaCursor(const TaArgs& a, const TaOwnPlan& p) {
-    const int per = p.head.heads * p.head.tiles, run = (int)blockIdx.x / per, j = (int)blockIdx.x % per;
-    head = j / p.head.tiles;
-    mt = j % p.head.tiles;
-    u = end = 0;
-    b = p.first_b;
-    if (run < p.head.runs) {
-      u = ta_run_start(p.head, run);
-      end = ta_run_start(p.head, run + 1);
-    }
-  }
+  QHL_DEV explicit TaCursor(const TaOwnPlan& p) : u(p.u), end(p.end), b(p.b), seg(p.seg), x(p.x) {}
   QHL_DEV bool next(const TaArgs& a, const TaOwnPlan& p, TaItem& w) {
+    const bool shared = p.head.tiles > 1;
     while (u < end) {
       if (a.n_batch <= kTaOwnPlan) {
         w.s = p.seq[b];
@@ -350,19 +362,23 @@ struct TaCursor {
         w.s = TaSeq{s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, 0};
       }
       const int units = ta_units(w.s);
-      const int at = u - w.s.base;
-      if (at >= ta_segments(w.s, p.head, a.Hkv) * units) {                      // behind its last segment, or it has none
+      if (units == 0 || seg >= p.head_groups * (shared ? 1 : w.s.nm)) {   // no segments, or behind the last
         ++b;
+        seg = x = 0;
         continue;
       }
-      const int seg = at / units, x = at - seg * units, y = min(units, x + (end - u));
-      u += y - x;
+      const int y = min(units, x + (end - u)), group = shared || w.s.nm == 1 ? seg : seg / w.s.nm;
       w.t0 = max(0, x - kTaStart);
       w.t1 = max(0, y - kTaStart);
-      const bool shared = p.head.tiles > 1;
-      w.h = (shared ? seg : seg / w.s.nm) * p.head.heads + head;
-      w.mt = shared ? mt : seg % w.s.nm;
+      w.h = group * p.head.heads + p.hd;
+      w.mt = shared ? p.mt : seg - group * w.s.nm;
       w.nct = (w.s.ctx + TaShape<DIM>::KT - 1) / TaShape<DIM>::KT;
+      u += y - x;
+      x = y;
+      if (y == units) {
+        ++seg;
+        x = 0;
+      }
       if (w.t1 > w.t0 && w.mt < w.s.nm) return true;
     }
     return false;
@@ -378,17 +394,17 @@ QHL_DEV void ta_own_plan(const TaArgs& a, TaOwnPlan& p) {
     if (tid < 32) {
       TaSeq s;
       const TaHead h = ta_plan_warp<KT>(a, s);
-      const int run = (int)blockIdx.x / (h.heads * h.tiles), u = run < h.runs ? ta_run_start(h, run) : 0;
       if (tid < a.n_batch) {
         p.seq[tid] = s;
         if (blockIdx.x == 0) a.seqs[tid] = s;
       }
-      const unsigned here = __ballot_sync(0xffffffffu, s.base <= u && u < s.base + (h.units ? ta_segments(s, h, a.Hkv) * ta_units(s) : 0));
       if (tid == 0) {
-        p.head = h;
-        p.first_b = here ? __ffs(here) - 1 : 0;
+        ta_set_run(a, h, p);
         if (blockIdx.x == 0) *a.head = h;
       }
+      __syncwarp();
+      const int u = p.u;
+      if (p.end > u && s.base <= u && u < s.base + ta_segments(s, h, a.Hkv) * ta_units(s)) ta_set_start(p, tid, s, u);
     }
     __syncthreads();
     return;
@@ -396,23 +412,21 @@ QHL_DEV void ta_own_plan(const TaArgs& a, TaOwnPlan& p) {
   const bool own = a.n_batch <= kTaOwnPlan;
   if (own) {
     const TaHead h = ta_plan<KT, kTaThreads / 32>(a, p.seq, p.scratch);
-    if (tid == 0) p.head = h;
+    if (tid == 0) ta_set_run(a, h, p);
     if (blockIdx.x == 0) {
       if (tid == 0) *a.head = h;
       if (tid < a.n_batch) a.seqs[tid] = p.seq[tid];
     }
   } else if (tid == 0) {
     const int4 h = __ldcg(reinterpret_cast<const int4*>(a.head));
-    p.head = TaHead{h.x, h.y, h.z, h.w};
+    ta_set_run(a, TaHead{h.x, h.y, h.z, h.w}, p);
   }
-  if (tid == 0) p.first_b = 0;
   __syncthreads();
   const TaHead h = p.head;
-  const int run = (int)blockIdx.x / (h.heads * h.tiles);
-  const int u = run < h.runs ? ta_run_start(h, run) : -1;
-  for (int b = tid; h.units && b < a.n_batch; b += kTaThreads) {
+  const int u = p.u;
+  for (int b = tid; p.end > u && b < a.n_batch; b += kTaThreads) {
     const TaSeq s = own ? p.seq[b] : a.seqs[b];
-    if (s.base <= u && u < s.base + ta_segments(s, h, a.Hkv) * ta_units(s)) p.first_b = b;
+    if (s.base <= u && u < s.base + ta_segments(s, h, a.Hkv) * ta_units(s)) ta_set_start(p, b, s, u);
   }
   __syncthreads();
 }
@@ -474,7 +488,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   pdl_wait();
   ta_own_plan<DIM>(a, s_plan);
-  TaCursor<DIM> cursor(a, s_plan);
+  TaCursor<DIM> cursor(s_plan);
   TaItem item;
   // Every wait is bounded; a role that gave one up stops (ok = false) once those
   // it shares a named barrier with know it too.
