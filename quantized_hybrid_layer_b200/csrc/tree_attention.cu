@@ -303,7 +303,8 @@ QHL_DEV float widen16(uint32_t h) {
 // A wait names a phase by its parity, so a waiter must not be two phases away
 // from it.  The softmax warps wait for the product with V only when they rescale
 // and at an item's end; pv_done is kept per tile parity for them: when S of tile
-// T is there, the product of tile T - 2, issued before it, is complete.
+// T is there, the product of tile T - 2, issued before it, is complete.  A slot of V
+// is empty when the product and warp 11, which looks at every tile, are done with it.
 struct TaBars {
   uint64_t full[12], empty[12], vok[12];
   uint64_t q_ready, s_full[2], p_ready[2], pv_done[2], mask_full, mask_empty;
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(bar(bars.full[i]), 1);
-      mbar_init(bar(bars.empty[i]), 1);
+      mbar_init(bar(bars.empty[i]), i & 1 ? 2 : 1);  // V's: the product and warp 11
       mbar_init(bar(bars.vok[i]), 1);
     }
     mbar_init(bar(bars.q_ready), 8);
@@ -688,12 +689,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
       if (lane == 0) mbar_arrive(bar(bars.mask_full));
 
       for (int tile = w.t0; ok && tile < w.t1; ++tile, r += 2) {
-        // every tile's V is waited for, so that the wait's parity is that of its phase
+        // every tile's V is waited for, and its slot is filled again only once this warp
+        // has been there, so that the wait's parity is that of its phase
         const bool draft = tile >= w.nct;
         const uint32_t s = r % NS;
         const int keys = ta_keys<KT>(w, tile);
         if (!(ok = wait_warp(bars.full[s], r / NS & 1))) break;
-        if (!draft && keys == KT) continue;
+        if (!draft && keys == KT) {
+          if (lane == 0) mbar_arrive(bar(bars.empty[s]));
+          continue;
+        }
         uint8_t* base = smem_raw + (ring + s * Sh::SLOT - smem_u32(smem_raw));
         // Rows up to the multiple of 16 that the product reads.  Units of 16 bytes;
         // the swizzle permutes the units of a row only.
@@ -723,7 +728,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bars.vok[s]));
+        if (lane == 0) {
+          mbar_arrive(bar(bars.vok[s]));
+          mbar_arrive(bar(bars.empty[s]));
+        }
       }
     }
   } else {
