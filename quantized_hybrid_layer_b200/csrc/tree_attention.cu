@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
   __shared__ __align__(16) uint4 s_anc[kMaxNodes];   // per token: the tokens it sees, a bit each
   __shared__ int s_jump[kMaxNodes];
   __shared__ unsigned s_bad[4];                      // tokens whose V row holds an infinity or NaN
+  __shared__ int s_gone;                             // whether the TMA warp has met a page that does not exist
   __shared__ float s_max[2][2][kTaRows], s_sum[2][kTaRows];
   __shared__ __align__(16) TaOwnPlan s_plan;
 
@@ -467,6 +468,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
       mbar_init(bar(bars.empty[i]), i & 1 ? 2 : 1);  // V's: the product and warp 11
       mbar_init(bar(bars.vok[i]), 1);
     }
+    s_gone = 0;
     mbar_init(bar(bars.q_ready), 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(bars.s_full[i]), 1);
@@ -521,6 +523,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
           if (pg < 0 || pg >= a.n_pages) {
             atomicOr(a.err, ERR_BAD_INDEX);
             pg = a.n_pages;                          // beyond the tensor: the copy fills zeros
+            s_gone = 1;                              // and the softmax warps, before they see the tile's S, learn of it
           }
         }
         return pg;
@@ -766,6 +769,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
       if (valid) anc = s_anc[node];
       const bool alive = (anc.x | anc.y | anc.z | anc.w) != 0;
       float m = -INFINITY, l = 0.f;
+      const int full = w.s.ctx / KT;                 // tiles of the cache that have all their keys
       bool stop = false;
 
       for (int tile = w.t0; tile < w.t1; ++tile, ++T) {
@@ -778,28 +782,38 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
         if (active) {
           tc_fence_after();
           const uint32_t sb = tmem + lanes + Sh::S0 + b * KT;
+          const int gone = s_gone;
           uint32_t sv[HK / 32][32];
 #pragma unroll
           for (int j = 0; j < HK / 32; ++j) tmem_ld32(sb + hf * HK + 32 * j, sv[j]);
           tmem_ld_wait();
-          if (tile >= w.nct) {
-            const int w0 = (tile - w.nct) * (KT / 32) + hf * (HK / 32);
+          if (tile >= full || gone) {                // perhaps not a tile of keys that all are seen
+            if (tile >= w.nct) {
+              const int w0 = (tile - w.nct) * (KT / 32) + hf * (HK / 32);
 #pragma unroll
-            for (int j = 0; j < HK / 32; ++j) {
-              const int wi = w0 + j;
-              const uint32_t bits = wi == 0 ? anc.x : wi == 1 ? anc.y : wi == 2 ? anc.z : anc.w;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(bits >> e & 1)) sv[j][e] = 0xff800000u;
-            }
-          } else {
-            const int lim = w.s.ctx - tile * KT - hf * HK;
-            if (lim < HK) {
-#pragma unroll
-              for (int j = 0; j < HK / 32; ++j)
+              for (int j = 0; j < HK / 32; ++j) {
+                const int wi = w0 + j;
+                const uint32_t bits = wi == 0 ? anc.x : wi == 1 ? anc.y : wi == 2 ? anc.z : anc.w;
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                  if (32 * j + e >= lim) sv[j][e] = 0xff800000u;
+                  if (!(bits >> e & 1)) sv[j][e] = 0xff800000u;
+              }
+            } else {
+              const int lim = w.s.ctx - tile * KT - hf * HK;
+#pragma unroll
+              for (int e = 0; e < HK; ++e)
+                if (e >= lim) sv[e / 32][e % 32] = 0xff800000u;
+              if (gone) {                            // pages have at least 16 rows
+                const int* row = a.table + (size_t)w.s.seq * a.max_pages;
+#pragma unroll
+                for (int e = 0; e < HK; e += 16) {
+                  const int key = tile * KT + hf * HK + e, pg = key < w.s.ctx ? __ldcg(row + (key >> a.page_shift)) : 0;
+                  if (pg < 0 || pg >= a.n_pages) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sv[(e + i) / 32][(e + i) % 32] = 0xff800000u;
+                  }
+                }
+              }
             }
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

@@ -16,3 +16,33 @@ def test_attention_many_laps_of_the_ring(q, dim, page, more):
     """Every CTA's run goes around the ring of tiles several times before the tiles that need care."""
     rows = 148 * 20 * (64 if dim == 256 else 128)
     check_attention(q, Trees([rows + more], [[-1, 0, 0]], 2, 1, dim, page, DTYPES["bf16"], seed=more))
+
+
+@pytest.mark.parametrize("dim,page,dtype", [(256, 16, "f16"), (256, 64, "bf16"), (128, 16, "bf16"), (128, 256, "f16"), (64, 32, "f16"), (64, 128, "bf16")])
+@pytest.mark.parametrize("which", ["first", "last", "middle", "several", "all"])
+def test_attention_rows_of_a_page_that_does_not_exist_are_absent(q, dim, page, dtype, which):  # noqa: F811
+    """A sequence with bad page numbers attends over its other rows; the call reports it."""
+    ctx = 3 * page + 450
+    t = Trees([ctx, 70], [[-1, 0, 0, -2], [-1]], 4, 2, dim, page, DTYPES[dtype], seed=dim + page)
+    s, n = int(t.seqs[0]), -(-ctx // page)
+    gone = {"first": [0], "last": [n - 1], "middle": [n // 2], "several": [0, 1, n // 2, n - 2], "all": list(range(n))}[which]
+    for i, p in enumerate(gone):
+        t.table[s, p] = (-1, int(t.refs.numel()), 2 ** 31 - 1, -2 ** 31)[i % 4]
+    keep = torch.tensor([r for r in range(ctx) if r // page not in gone], dtype=torch.long)
+    t.K[0], t.V[0] = t.K[0][keep], t.V[0][keep]
+    with pytest.raises(q.StageError) as e:
+        check_attention(q, t)                            # its last line is the report
+    assert e.value.code == -7
+
+
+def test_attention_pages_that_do_not_exist_in_a_long_run_of_small_ones(q):  # noqa: F811
+    """Bad pages here and there among thousands, many to a CTA's run."""
+    page, ctx = 16, 148 * 300
+    t = Trees([ctx], [random_tree(5, gen(2))], 2, 1, 256, page, torch.float16, seed=12)
+    gone = torch.randperm(ctx // page, generator=gen(3))[:400]
+    t.table[0, gone] = -1
+    keep = ~torch.isin(torch.arange(ctx) // page, gone)
+    t.K[0], t.V[0] = t.K[0][keep], t.V[0][keep]
+    with pytest.raises(q.StageError) as e:
+        check_attention(q, t)
+    assert e.value.code == -7
