@@ -215,8 +215,10 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 v = heads_of(a[12], "v", dev, dt, hkv, dim, rows);
     if (rows > INT32_MAX || width > INT32_MAX) refuse("y is too large");
     if (rows == 0) return 0;
+    // the stride of one row alone is never used: any that the checks accept will do
+    const long long stride = rows > 1 ? y.stride(0) : (width + 7) / 8 * 8;
     const On o(dev, a[16]);
-    return g_lib.norm_rope(hq, hkv, dim, rope, theta, eps, y.data_ptr(), yt, rows > 1 ? y.stride(0) : width, (int)off[0], (int)off[1],
+    return g_lib.norm_rope(hq, hkv, dim, rope, theta, eps, y.data_ptr(), yt, stride, (int)off[0], (int)off[1],
                            (int)off[2], (int)rows, pos, gq, gk, dt, q.p, q.stride, k.p, k.stride, v.p, v.stride, o.stream);
   });
 }

@@ -46,3 +46,22 @@ def test_attention_pages_that_do_not_exist_in_a_long_run_of_small_ones(q):  # no
     with pytest.raises(q.StageError) as e:
         check_attention(q, t)
     assert e.value.code == -7
+
+
+# ------------------------------------------------------------- norm and rope
+
+@pytest.mark.parametrize("src", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n", [1, 2])
+def test_norm_rope_of_a_view_whose_width_is_not_a_multiple_of_16_bytes(q, src, n):  # noqa: F811
+    """One row of padded rows is as good as two: the width of a view is no stride."""
+    st = {"f32": torch.float32, **DTYPES}[src]
+    full = torch.randn(n, 1024, generator=gen(n)).to(st).cuda()
+    pos, one = torch.arange(n, dtype=torch.int32, device="cuda"), torch.ones(64, device="cuda")
+
+    def run(y):
+        out = [torch.zeros(n, h, 64, dtype=torch.float16, device="cuda") for h in (4, 2, 2)]
+        return q.qhl_qk_norm_rope(4, 2, 64, 64, 1e4, 1e-6, y, pos, one, one, *out, offsets=(0, 512, 768))
+
+    want = run(full)
+    for width in (897, 898, 1023):                       # the last head ends at 896
+        assert all(torch.equal(a, b) for a, b in zip(run(full[:, :width]), want))
