@@ -454,8 +454,9 @@ class KvPages:
 
     def __init__(self, k, v, table, lens, held, refs):
         dtype = {"torch.float16": QHL_F16, "torch.bfloat16": QHL_BF16}.get(str(k.dtype))
-        if not (k.dim() == 5 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype and k.device == v.device
-                and k.stride(4) == 1 and dtype is not None):
+        # the stride along an axis of one element is never used
+        if not (k.dim() == 5 and k.shape == v.shape and all(n == 1 or a == b for n, a, b in zip(k.shape, k.stride(), v.stride()))
+                and k.dtype == v.dtype and k.device == v.device and k.stride(4) == 1 and dtype is not None):
             raise ValueError("k and v must be alike, float16 or bfloat16 [layers, pages, kv_heads, page_rows, dim] with contiguous "
                              f"elements, got {k.dtype} {list(k.shape)} strides {k.stride()} on {k.device} and {v.dtype} {list(v.shape)} "
                              f"strides {v.stride()} on {v.device}")
@@ -468,7 +469,7 @@ class KvPages:
                 raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {k.device}, got {t.dtype} {list(t.shape)} on {t.device}")
         self.k, self.v, self.table, self.lens, self.held, self.refs = k, v, table, lens, held, refs
         self.layers, self.pages, self.kv_heads, self.page_rows, self.dim, self.seqs, self.max_pages = L, N, H, P, D, S, M
-        # the stride along an axis of one element is never used: any that the checks accept will do
+        # any stride along an axis of one element that the checks accept will do
         st = [k.stride(a) if k.shape[a] > 1 else max(D, 8) for a in range(4)]
         self._c = KvPagesStruct(k.data_ptr(), v.data_ptr(), dtype, L, N, H, P, D, st[0], st[1], st[2], st[3], S, M, table.data_ptr(),
                                 lens.data_ptr(), held.data_ptr(), refs.data_ptr())

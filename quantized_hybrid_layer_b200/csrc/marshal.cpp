@@ -332,8 +332,10 @@ PyObject* pages_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
           (t->numel() > 0 && (t->stride(3) != 1 || (kv->kv_heads > 1 && t->stride(2) != kv->dim))))
         refuse("k_new and v_new must be [" + std::to_string(kv->n_layers) + ", rows, " + std::to_string(kv->kv_heads) + ", " +
                std::to_string(kv->dim) + "] in the cache's type with contiguous heads on its device, " + describe(*t));
-    if (k.sizes() != v.sizes() || k.strides() != v.strides()) refuse("k_new and v_new must be alike");
-    const long long rows = k.size(1), sr = rows > 1 ? k.stride(1) : (long long)kv->kv_heads * kv->dim, sl = kv->n_layers > 1 ? k.stride(0) : sr;
+    const long long rows = k.size(1);
+    if (v.size(1) != rows || (rows > 1 && k.stride(1) != v.stride(1)) || (kv->n_layers > 1 && k.stride(0) != v.stride(0)))
+      refuse("k_new and v_new must be alike");
+    const long long sr = rows > 1 ? k.stride(1) : (long long)kv->kv_heads * kv->dim, sl = kv->n_layers > 1 ? k.stride(0) : sr;
     const int *s = ints(a[2], "seqs", dev, b), *start = ints(a[3], "q_start", dev, b + 1), *acc = ints(a[5], "n_accepted", dev, b),
               *pos = ints(a[6], "pos", dev, b);
     const int* path = dense<int>(a[4], "path", dev, at::kInt, {b, pt.size(1)});

@@ -65,3 +65,24 @@ def test_norm_rope_of_a_view_whose_width_is_not_a_multiple_of_16_bytes(q, src, n
     want = run(full)
     for width in (897, 898, 1023):                       # the last head ends at 896
         assert all(torch.equal(a, b) for a, b in zip(run(full[:, :width]), want))
+
+
+# --------------------------------------------------------------------- pages
+
+def test_strides_along_an_axis_of_one_element_do_not_count(q):  # noqa: F811
+    """A cache of one layer cut out of a larger one, and one drafted row of every layer: k and v may come from tensors of
+    other sizes as long as the strides that are used agree."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")   # noqa: E731
+    half = lambda *s: torch.randn(s, generator=gen(1)).half().cuda()   # noqa: E731
+    k, v = half(3, 4, 2, 16, 64)[1:2], half(1, 4, 2, 16, 64)
+    assert k.stride(1) == v.stride(1)
+    v3 = torch.as_strided(v, v.shape, (8, *v.stride()[1:]))
+    kv = q.KvPages(k, v3, i32(1, 2), i32(1) + 4, i32(1) + 1, i32(4) + 1)
+    new_k, new_v = half(1, 1, 2, 64), half(2, 3, 2, 64)[:1, 1:2]
+    assert new_k.stride() != new_v.stride()
+    status = i32(1) + 9
+    starts = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    q.qhl_pages_commit(kv, i32(1), starts, i32(1, 1), i32(1) + 1, i32(1) + 4, new_k, new_v, status)
+    assert status.tolist() == [0] and kv.lens.tolist() == [5]
+    assert torch.equal(k[0, 0, :, 4], new_k[0, 0]) and torch.equal(v[0, 0, :, 4], new_v[0, 0])
+    q.qhl_sync()
