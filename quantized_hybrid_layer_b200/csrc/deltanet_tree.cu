@@ -82,7 +82,7 @@ QHL_DEV float4 ld_after_stores(const float* p) {
 // most 32: the CTAs of a large tree then do not start last.  A full warp calls it.
 QHL_DEV int tree_by_size(const int* q_start, int n_batch, int rank) {
   const int lane = threadIdx.x & 31;
-  const int size = lane < n_batch ? __ldg(q_start + lane + 1) - __ldg(q_start + lane) : INT_MIN;
+  const int size = lane < n_batch ? q_start[lane + 1] - q_start[lane] : INT_MIN;
   int before = 0;
   for (int i = 0; i < n_batch; ++i) {
     const int o = __shfl_sync(0xffffffffu, size, i);
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(ROWS / R * 32, PER_SM) dn_tree_kernel(const Dn
   pdl_wait();
   int first, n;
   const int tree = a.n_batch > 1 && a.n_batch <= 32 ? tree_by_size(a.q_start, a.n_batch, blockIdx.y) : (int)blockIdx.y;
-  int idx = __ldg(a.index + tree);
+  int idx = a.index[tree];
   tree_rows(a.q_start, tree, a.n_rows, a.max_nodes, first, n, a.err);
   if (n == 0) return;
 
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(ROWS / R * 32, PER_SM) dn_tree_kernel(const Dn
       copy_async4(tid & 1 ? &s.a[t] : &s.b[t], y + (size_t)t * a.y_stride + (tid & 1 ? off_a : off_b) + h);
     }
   };
+  int parent = tid < n ? a.parent[first + tid] : -2;
   stage_in(stage[0], 0);
-  int parent = tid < n ? __ldg(a.parent + first + tid) : -2;
   if (idx < -1 || idx >= a.n_states) {
     if (tid == 0) atomicOr(a.err, ERR_BAD_INDEX);
     idx = -1;

@@ -99,13 +99,13 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeArgs a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       raw[u][j] = typename Pack<SRC>::V{};
-      if (vec < nvec) raw[u][j] = __ldg(reinterpret_cast<const typename Pack<SRC>::V*>(yr + off + j * (D / 2)));
+      if (vec < nvec) raw[u][j] = *reinterpret_cast<const typename Pack<SRC>::V*>(yr + off + j * (D / 2));
     }
   }
 
   const int half = a.rope / 2;
   if (v0 < a.hq + a.hkv && half) {
-    const double pos = (double)__ldg(a.pos + row);
+    const double pos = (double)a.pos[row];
     for (int i = lane; i < half; i += 32) {
       double f = 1.0;
 #pragma unroll
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeArgs a) {
       if (kind < 2) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float4 g = __ldg(reinterpret_cast<const float4*>((kind == 0 ? a.gq : a.gk) + d0 + j * (D / 2)));
+          const float4 g = *reinterpret_cast<const float4*>((kind == 0 ? a.gq : a.gk) + d0 + j * (D / 2));
           x[j][0] *= r * g.x; x[j][1] *= r * g.y; x[j][2] *= r * g.z; x[j][3] *= r * g.w;
         }
       }

@@ -133,7 +133,7 @@ QHL_DEV int held_of(const PagesView& p, int s) {
 // CTA call it and get the answer).
 QHL_DEV bool named_before(const int* seq, int i, int s) {
   bool dup = false;
-  for (int j = threadIdx.x; j < i; j += blockDim.x) dup |= __ldg(seq + j) == s;
+  for (int j = threadIdx.x; j < i; j += blockDim.x) dup |= seq[j] == s;
   return __syncthreads_or(dup);
 }
 
@@ -142,7 +142,7 @@ QHL_DEV bool named_before(const int* seq, int i, int s) {
 __global__ void __launch_bounds__(128) pages_free_kernel(const PagesView p, const int* seq, int* status) {
   if (threadIdx.x == 0) pdl_launch();
   pdl_wait();
-  const int i = blockIdx.x, s = __ldg(seq + i);
+  const int i = blockIdx.x, s = seq[i];
   const bool dup = named_before(seq, i, s);
   if (s < 0 || s >= p.n_seqs || dup) {
     if (threadIdx.x == 0) status[i] = STAGE_E_ARG;
@@ -171,10 +171,10 @@ __global__ void __launch_bounds__(128) pages_free_kernel(const PagesView p, cons
 __global__ void __launch_bounds__(128) pages_fork_kernel(const PagesView p, int n, const int* src, const int* dst, int* status) {
   if (threadIdx.x == 0) pdl_launch();
   pdl_wait();
-  const int i = blockIdx.x, s = __ldg(src + i), d = __ldg(dst + i);
+  const int i = blockIdx.x, s = src[i], d = dst[i];
   bool again = false;   // dst named before, or src a dst of this call
   for (int j = threadIdx.x; j < n; j += 128) {
-    const int o = __ldg(dst + j);
+    const int o = dst[j];
     again |= (j < i && o == d) || o == s;
   }
   again = __syncthreads_or(again);
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(1024) pages_extend_kernel(const PagesView p, i
   const int tid = threadIdx.x, P = p.rows;
   if (tid == 0) pdl_launch();
   pdl_wait();
-  const int s = tid < n ? __ldg(seq + tid) : -1;
-  const int more = tid < n ? __ldg(add + tid) : 0;
+  const int s = tid < n ? seq[tid] : -1;
+  const int more = tid < n ? add[tid] : 0;
   s_seq[tid] = s;
   __syncthreads();
   int rc = STAGE_OK, len = 0, held = 0, want = 0, last_at = 0, last = -1, refs = 0;
@@ -423,12 +423,13 @@ __global__ void __launch_bounds__(256) pages_commit_kernel(const PagesView p, co
   const int b = blockIdx.x, tid = threadIdx.x, layer = blockIdx.y >> 1, P = p.rows;
   if (tid == 0) pdl_launch();
   pdl_wait();
-  const int s = __ldg(a.seq + b);
-  if (tid == 0) s_arg = s_state = 0;
-  const bool dup = named_before(a.seq, b, s);
+  // all that does not depend on another load goes out at once
+  const int s = a.seq[b], acc = a.n_accepted[b], pos = a.pos[b];
+  const int node = tid < min(a.path_stride, kMaxNodes) ? a.path[(size_t)b * a.path_stride + tid] : -1;
   int first, n;
   tree_rows(a.q_start, b, a.n_rows, kMaxNodes, first, n, p.err);
-  const int acc = __ldg(a.n_accepted + b), pos = __ldg(a.pos + b);
+  if (tid == 0) s_arg = s_state = 0;
+  const bool dup = named_before(a.seq, b, s);
   int rc = STAGE_OK;
   if (s < 0 || s >= p.n_seqs || dup || acc < 0 || acc > min(a.path_stride, kMaxNodes) || pos < 0) {
     rc = STAGE_E_ARG;
@@ -437,7 +438,6 @@ __global__ void __launch_bounds__(256) pages_commit_kernel(const PagesView p, co
   } else if ((long long)pos + acc > (long long)held_of(p, s) * P) {
     rc = STAGE_E_STATE;
   } else if (tid < acc) {
-    const int node = __ldg(a.path + (size_t)b * a.path_stride + tid);
     const int page = p.table[(size_t)s * p.max_pages + (pos + tid) / P];
     if (node < 0 || node >= n) {
       rc = STAGE_E_ARG;

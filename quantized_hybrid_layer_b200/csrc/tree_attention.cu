@@ -146,7 +146,7 @@ QHL_DEV int ta_run_of(const TaHead& h, int u) {
 template <int KT>
 QHL_DEV TaSeq ta_seq(const TaArgs& a, int b) {
   TaSeq s;
-  s.seq = __ldg(a.seq + b);
+  s.seq = a.seq[b];
   tree_rows(a.q_start, b, a.n_rows, a.max_nodes, s.row0, s.n, a.err);
   s.ctx = 0;
   if (s.seq < 0 || s.seq >= a.n_seqs) {
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
       auto page_of = [&](int j) {
         int pg = -1;
         if (j < box_end) {
-          pg = __ldg(row + (j >> (a.page_shift - a.box_shift)));
+          pg = row[j >> (a.page_shift - a.box_shift)];
           if (pg < 0 || pg >= a.n_pages) {
             atomicOr(a.err, ERR_BAD_INDEX);
             pg = a.n_pages;                          // beyond the tensor: the copy fills zeros
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
       // ancestors by doubling: after k rounds those up to 2^k steps away; a jump
       // ends at -1 (the cached sequence) or -2 (padded: nothing is seen)
       for (int x = lane; x < n; x += 32) {
-        int p = __ldg(a.parent + w.s.row0 + x);
+        int p = a.parent[w.s.row0 + x];
         if (p < -2 || p >= x) {
           atomicOr(a.err, ERR_BAD_INDEX);
           p = -2;
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
         for (int j = 0; j < DIM / 64; ++j) {         // 32 elements, 16 columns
           uint4 x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = valid ? __ldg(src + 4 * j + e) : make_uint4(0, 0, 0, 0);
+          for (int e = 0; e < 4; ++e) x[e] = valid ? src[4 * j + e] : make_uint4(0, 0, 0, 0);
           tmem_st16(tmem + lanes + Sh::Q0 + hf * (DIM / 4) + 16 * j, reinterpret_cast<const uint32_t*>(x));
         }
         tmem_st_wait();
@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
                 const int* row = a.table + (size_t)w.s.seq * a.max_pages;
 #pragma unroll
                 for (int e = 0; e < HK; e += 16) {
-                  const int key = tile * KT + hf * HK + e, pg = key < w.s.ctx ? __ldcg(row + (key >> a.page_shift)) : 0;
+                  const int key = tile * KT + hf * HK + e, pg = key < w.s.ctx ? row[key >> a.page_shift] : 0;
                   if (pg < 0 || pg >= a.n_pages) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) sv[(e + i) / 32][(e + i) % 32] = 0xff800000u;
@@ -920,7 +920,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attn_kernel(const __grid_c
               const uint16_t* vr = static_cast<const uint16_t*>(a.v_new) + (long long)(w.s.row0 + x) * a.new_stride + w.h * DIM + hf * (DIM / 2) + 32 * j;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const uint32_t h = __ldg(vr + e);
+                const uint32_t h = vr[e];
                 if (non_finite16<BF16>(h)) o[e] = __float_as_uint(__uint_as_float(o[e]) + widen16<BF16>(h));
               }
             }

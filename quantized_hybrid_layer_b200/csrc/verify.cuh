@@ -54,7 +54,7 @@ int check_pages(const char* call, const qhl_kv_pages* kv);
 // Rows [first, first + n) of tree b, or n = 0 (and the error bit) where q_start
 // does not fit the call's n_rows and max_nodes.
 QHL_DEV void tree_rows(const int* q_start, int b, int n_rows, int max_nodes, int& first, int& n, unsigned* err) {
-  const int a = __ldg(q_start + b), e = __ldg(q_start + b + 1);
+  const int a = q_start[b], e = q_start[b + 1];
   first = a;
   n = e - a;
   if (a < 0 || e < a || e > n_rows || n > max_nodes) {

@@ -2,6 +2,8 @@
 calls' argument checks, the binding's, and the plain page operations that the
 GPU tests compare with."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -156,3 +158,13 @@ def test_plain_page_operations():
     assert p.extend([0, 0, 3, 3], [99, 1, -1, 0]) == [E_ARG, E_ARG, E_ARG, E_ARG]
     assert p.free([2, 2, 7]) == [OK, E_ARG, E_ARG]
     assert p.refs == [2, 1, 1, 0, 0, 0]
+
+
+def test_kernels_that_start_before_their_predecessor_ends_use_coherent_loads():
+    """A non-coherent load (__ldg, ld.global.nc) promises that its data does not change while the kernel runs; these kernels
+    run beside the one that writes their inputs until they have waited for it."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "quantized_hybrid_layer_b200", "csrc")
+    for name in ("norm_rope.cu", "tree_attention.cu", "deltanet_tree.cu", "pages.cu", "verify.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        assert not re.search(r"__ldg\b|\.nc\b|__restrict__", text), name
