@@ -211,30 +211,34 @@ struct PageCopy {
   int from, to, rows, pad;
 };
 
-// Sum of v over the threads before this one; `total`: over all.  1024 threads.
-QHL_DEV int block_scan(int v, int* warp_sums, int& total) {
+// Sum of v over the threads up to this one; `total`: over all.  1024 threads.  v is at
+// most 2^26 + 1, more than a pool's pages.  A sum above kScanMost comes out as some
+// number of at least kScanMost: a warp's sum fits 32 bits, and so do 32 of kScanMost.
+constexpr unsigned kScanMost = (1u << 27) - 1;
+QHL_DEV int block_scan(int v, unsigned* warp_sums, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+  unsigned inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    const unsigned u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
+  inc = min(inc, kScanMost);
   __syncthreads();
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    int w = warp_sums[lane];
+    unsigned w = warp_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, o);
+      const unsigned u = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += u;
     }
-    warp_sums[lane] = w;
+    warp_sums[lane] = min(w, kScanMost);
   }
   __syncthreads();
   total = warp_sums[31];
-  return inc - v + (warp ? warp_sums[warp - 1] : 0);
+  return inc + (warp ? warp_sums[warp - 1] : 0);
 }
 
 // Requests i = thread.  A request needs `copied` (0 or 1) + `fresh` pages; the
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(1024) pages_extend_kernel(const PagesView p, i
                                                             PageCopy* copies) {
   __shared__ int s_seq[kMaxRequests], s_last[kMaxRequests], s_end[kMaxRequests], s_at[kMaxRequests], s_copied[kMaxRequests],
       s_held[kMaxRequests];
-  __shared__ int s_warp[32];
+  __shared__ unsigned s_warp[32];
   const int tid = threadIdx.x, P = p.rows;
   if (tid == 0) pdl_launch();
   pdl_wait();
@@ -298,10 +302,9 @@ __global__ void __launch_bounds__(1024) pages_extend_kernel(const PagesView p, i
     }
     fresh = max(0, want - held);
   }
-  const int need = copied + fresh;
+  const int need = min(copied + fresh, p.n_pages + 1);   // the pool's size is not enough for either
   int total;
-  const int begin = block_scan(need, s_warp, total);
-  s_end[tid] = begin + need;
+  s_end[tid] = block_scan(need, s_warp, total);
   s_at[tid] = last_at;                       // table index of the page that is copied
   s_copied[tid] = copied;
   s_held[tid] = held;
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(1024) pages_extend_kernel(const PagesView p, i
   int rank = 0;
   for (long long base = 0; base < p.n_pages && have < total; base += kSweep) {
     bits = free_of(base);
-    rank = block_scan(__popc(bits), s_warp, sweep_free);
+    rank = block_scan(__popc(bits), s_warp, sweep_free) - __popc(bits);
     have += sweep_free;
   }
   __syncthreads();
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(1024) pages_extend_kernel(const PagesView p, i
   for (long long base = 0; base < p.n_pages && given < min(have, total); base += kSweep) {
     if (p.n_pages > kSweep) {
       bits = free_of(base);
-      rank = block_scan(__popc(bits), s_warp, sweep_free);
+      rank = block_scan(__popc(bits), s_warp, sweep_free) - __popc(bits);
     }
     int f = given + rank;
     for (unsigned left = bits; left && f < total; left &= left - 1, ++f) {

@@ -86,3 +86,22 @@ def test_strides_along_an_axis_of_one_element_do_not_count(q):  # noqa: F811
     assert status.tolist() == [0] and kv.lens.tolist() == [5]
     assert torch.equal(k[0, 0, :, 4], new_k[0, 0]) and torch.equal(v[0, 0, :, 4], new_v[0, 0])
     q.qhl_sync()
+
+
+def test_pages_needs_beyond_32_bits_are_refused(q):  # noqa: F811
+    """34 requests of 2^27 pages each: their sum passes 2^31 and 2^32, the pool has eight."""
+    S, most = 34, 1 << 27
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")   # noqa: E731
+    pool = torch.zeros(1, 8, 1, 16, 64, dtype=torch.float16, device="cuda")
+    table = torch.empty(S, most, dtype=torch.int32, device="cuda")       # 17 GB, of which nothing is read
+    kv = q.KvPages(pool, pool.clone(), table, i32(S), i32(S), i32(8))
+    seqs, status = torch.arange(S, dtype=torch.int32, device="cuda"), i32(S) + 9
+    add = torch.full((S,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    q.qhl_pages_extend(kv, seqs, add, status)
+    assert status.tolist() == [-3] * S
+    assert kv.held.tolist() == [0] * S and kv.refs.tolist() == [0] * 8
+    add[0] = 100                                         # what the pool has goes to the requests before the one that fails
+    q.qhl_pages_extend(kv, seqs, add, status)
+    assert status.tolist() == [0] + [-3] * (S - 1)
+    assert kv.held.tolist() == [7] + [0] * (S - 1) and kv.refs.tolist() == [1] * 7 + [0] and table[0, :7].tolist() == list(range(7))
+    q.qhl_sync()
