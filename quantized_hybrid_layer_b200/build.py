@@ -10,10 +10,12 @@ becomes an extension module of its own, so the library stays free of PyTorch.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -33,10 +35,11 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _deps_mtime() -> float:
-    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+def _stale(out: str, marshal: bool) -> bool:
+    """Whether `out` is older than a source of it: marshal.cpp, or all the others, and the header."""
+    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if (f == "marshal.cpp") == marshal]
     paths.append(os.path.join(os.path.dirname(HERE), "include", "qhl_stage.h"))
-    return max(os.path.getmtime(p) for p in paths)
+    return not os.path.exists(out) or os.path.getmtime(out) < max(os.path.getmtime(p) for p in paths)
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -52,11 +55,13 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _build_marshal():
-    import sysconfig
+def _torch_root() -> str | None:
+    """Where PyTorch is installed, if it is (it is not imported: that takes seconds)."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
-    import torch
-    root = os.path.dirname(torch.__file__)
+
+def _build_marshal(root: str):
     include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     tmp = MARSHAL + f".tmp{os.getpid()}"
@@ -68,19 +73,32 @@ def _build_marshal():
     os.replace(tmp, MARSHAL)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime() for p in (LIB, MARSHAL)):
-        return LIB
+def _build_lib(verbose: bool):
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        marshal = ex.submit(_build_marshal)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        marshal.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """The library, and the marshalling module beside it.  The library needs nvcc alone: it is there even where the module
+    cannot be built, which is left out where PyTorch or g++ is missing."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        marshal = None
+        if force or _stale(MARSHAL, True):
+            root = _torch_root()
+            if root and shutil.which("g++"):
+                marshal = ex.submit(_build_marshal, root)
+            else:
+                sys.stderr.write(f"{'g++' if root else 'PyTorch'} is missing: the Python binding's tree-verification calls are not built\n")
+        if force or _stale(LIB, False):
+            _build_lib(verbose)
+        if marshal:
+            marshal.result()
     return LIB
 
 
