@@ -10,6 +10,7 @@ becomes an extension module of its own, so the library stays free of PyTorch.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -61,12 +62,28 @@ def _torch_root() -> str | None:
     return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
+def _built_for() -> str:
+    """What the marshalling module is built against; its docstring holds it, so that a module for another is known as one."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:      # on the path, but not installed as a package
+        version = "of unknown version"
+    return f"built for torch {version}, {sysconfig.get_config_var('SOABI')}"
+
+
+def _marshal_stale() -> bool:
+    if _stale(MARSHAL, True):
+        return True
+    with open(MARSHAL, "rb") as f:
+        return _built_for().encode() not in f.read()
+
+
 def _build_marshal(root: str):
     include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     tmp = MARSHAL + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG", *[f"-I{p}" for p in include], os.path.join(CSRC, "marshal.cpp"),
-           "-o", tmp, f"-L{root}/lib", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{root}/lib"]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG", f'-DQHL_BUILT_FOR="{_built_for()}"', *[f"-I{p}" for p in include],
+           os.path.join(CSRC, "marshal.cpp"), "-o", tmp, f"-L{root}/lib", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{root}/lib"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stderr}")
@@ -89,8 +106,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     cannot be built, which is left out where PyTorch or g++ is missing."""
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
         marshal = None
-        if force or _stale(MARSHAL, True):
-            root = _torch_root()
+        root = _torch_root()
+        if force or not root or _marshal_stale():
             if root and shutil.which("g++"):
                 marshal = ex.submit(_build_marshal, root)
             else:

@@ -362,7 +362,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind),       FAST(norm_rope),    FAST(tree_attention), FAST(deltanet_tree), FAST(pages_free),
                          FAST(pages_fork), FAST(pages_extend), FAST(pages_commit),   {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "Native marshalling of the tree-verification calls.", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "Native marshalling of the tree-verification calls, " QHL_BUILT_FOR ".", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

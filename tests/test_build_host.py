@@ -1,4 +1,5 @@
 """What build.py builds and when, with compilers that only write their output files."""
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -77,3 +78,12 @@ def test_each_is_rebuilt_for_its_own_sources(fake):
     os.utime(fake.marshal, (later, later))
     os.utime(os.path.join(fake.src, "pages.cu"), (later, later))
     assert built(fake) == sorted(b.SOURCES + ["link"])
+
+
+def test_the_marshalling_module_is_rebuilt_for_another_pytorch(fake, monkeypatch):
+    built(fake)
+    assert built(fake) == []
+    version = importlib.metadata.version
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "99.1" if name == "torch" else version(name))
+    assert built(fake) == ["g++"]
+    assert built(fake) == []
