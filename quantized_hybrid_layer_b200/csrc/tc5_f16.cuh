@@ -31,16 +31,9 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, bool b_mn_major, int
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D[tmem] (=|+=) A * B^T over K = 16, A in shared memory (ss) or in tensor
-// memory (ts: row m in lane m, two elements of K to a column).  Asynchronous,
-// issued by one thread; completion through tc_commit.
-QHL_DEV void mma_f16_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
-      : "memory");
-}
+// D[tmem] (=|+=) A * B^T over K = 16, A in tensor memory (row m in lane m, two
+// elements of K to a column), B in shared memory.  Asynchronous, issued by one
+// thread; completion through tc_commit.
 QHL_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
