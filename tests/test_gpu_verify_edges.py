@@ -1,9 +1,11 @@
 """The tree-verification operators on the GPU: the forms, sizes and calls that only a served batch or a long cache reaches."""
+import math
+
 import pytest
 import torch
 
-from test_gpu_verify import check_attention, q  # noqa: F401  (q is a fixture)
-from verify_helpers import DTYPES, Trees, gen, random_tree
+from test_gpu_verify import check_attention, q, run_attention  # noqa: F401  (q is a fixture)
+from verify_helpers import DTYPES, Trees, gen, half_step, random_tree, tiny_step
 
 pytestmark = pytest.mark.gpu
 
@@ -46,6 +48,53 @@ def test_attention_pages_that_do_not_exist_in_a_long_run_of_small_ones(q):  # no
     with pytest.raises(q.StageError) as e:
         check_attention(q, t)
     assert e.value.code == -7
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_attention_a_long_cache_of_values_of_one_sign(q, dtype, dim):  # noqa: F811
+    """Values with a mean, so that a part that is lost or counted twice shows; the weights' subnormal numbers count 2^-31."""
+    t = Trees([9001], [random_tree(4, gen(1))], 4, 2, dim, 64, DTYPES[dtype], seed=8)
+    t.V[0], t.v_new = (1 + 0.2 * t.V[0].float()).to(t.dtype), (1 + 0.2 * t.v_new.float()).to(t.dtype)
+    s = int(t.seqs[0])
+    for j in range(-(-9001 // 64)):
+        m = min(64, 9001 - 64 * j)
+        t.v[0, int(t.table[s, j]), :, :m] = t.V[0][64 * j:64 * j + m].transpose(0, 1)
+    out, _ = run_attention(q, t)
+    ref, _, tol, _ = t.reference(subnormal=2.0 ** -31)
+    assert bool(((out.double() - ref).abs() <= tol).all())
+    q.qhl_sync()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention_f16_weights_of_a_long_tail_are_kept(q, dim):  # noqa: F811
+    """One key in 64 has nearly all the weight and values of 0, the others less than 2^-25 of it each and values of 1024: alone,
+    such a weight rounds to 0 in f16."""
+    n, P = 9000, 64
+    t = Trees([n], [[-1]], 1, 1, dim, P, torch.float16, seed=5)
+    g = gen(31)
+    score = -25.5 * math.log(2) + 0.4 * (torch.rand(n, generator=g) - 0.5)
+    score[::64] = 0
+    t.q.zero_(), t.k_new.zero_(), t.v_new.zero_()
+    t.q[:, :, 0] = math.sqrt(dim)                        # the scale undoes it: a key's first element is its score
+    t.K[0] = torch.zeros(n, 1, dim, dtype=torch.float16)
+    t.K[0][:, 0, 0] = score.half()
+    t.V[0] = torch.where(score == 0, 0.0, 1024.0)[:, None, None].expand(n, 1, dim).half()
+    s = int(t.seqs[0])
+    for j in range(-(-n // P)):
+        m = min(P, n - P * j)
+        t.k[0, int(t.table[s, j]), :, :m] = t.K[0][P * j:P * j + m].transpose(0, 1)
+        t.v[0, int(t.table[s, j]), :, :m] = t.V[0][P * j:P * j + m].transpose(0, 1)
+    out, _ = run_attention(q, t)
+    w = torch.softmax(torch.cat([t.K[0][:, 0, 0].double(), torch.zeros(1, dtype=torch.float64)]), 0)
+    ref = float((w[:n] * t.V[0][:, 0, 0].double()).sum())
+    # every part of the sum has its own largest key, so a weight's half step is 2^-31 of a sum of at least n / 64 (+ 1 drafted):
+    # n 2^-31 1024 / (n / 64); the scores are exact products, 2^-22 of 18 for the exponent; u for normal weights and the result
+    u = half_step(torch.float16)
+    tol = 64 * 2.0 ** -31 * 1024 + ref * (2.02 * u + 2 * 18 * 2.0 ** -22 + (n + 16) * 2.0 ** -23) + tiny_step(torch.float16)
+    assert tol < 0.05 * ref
+    assert bool(((out.double() - ref).abs() <= tol).all())
+    q.qhl_sync()
 
 
 # ------------------------------------------------------------- norm and rope

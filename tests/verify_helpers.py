@@ -90,7 +90,7 @@ class Trees:
         self.v_new = torch.randn(self.rows, kv_heads, dim, generator=g).to(dtype)
         self.scale = 1 / math.sqrt(dim)
 
-    def reference(self):
+    def reference(self, subnormal=2.0 ** -25):
         """(out, lse, tolerance of out, tolerance of lse) in 64 bits, for the rows of the trees.
 
         The kernel's errors, in units of u = half a step of the 16-bit type and of f32's 2^-24:
@@ -99,7 +99,10 @@ class Trees:
         rounding of the exponent's product, 2^-23 |s| log2 e; a weight is off by a factor within
         e^(2 ds) and, rounded for the product with v, by u (or, for f16, by half a subnormal step,
         2^-25, where weights are at least 1 in sum); the sum over n keys adds n 2^-23; the result is
-        rounded by u."""
+        rounded by u.
+
+        subnormal: that half step, in units of the largest weight.  The kernel's weights are 2^6
+        larger than their softmax numerators, so it keeps to 2^-31 as well."""
         G, D = self.heads // self.kv_heads, self.dim
         u = half_step(self.dtype)
         out = torch.zeros(self.rows, self.heads, D, dtype=torch.float64)
@@ -124,7 +127,7 @@ class Trees:
                     out[a + i, j] = w @ vv
                     lse[a + i, j] = torch.logsumexp(s, 0)
                     A = w @ vv.abs()
-                    sub = n * 2.0 ** -25 * float(vv.abs().max()) if self.dtype == torch.float16 else 0.0
+                    sub = n * subnormal * float(vv.abs().max()) if self.dtype == torch.float16 else 0.0
                     tol[a + i, j] = u * out[a + i, j].abs() + A * (1.01 * u + 2.5 * ds + (n + 16) * 2.0 ** -23) + sub + tiny_step(self.dtype)
                     ltol[a + i, j] = 1.5 * ds + (n + 16) * 2.0 ** -23 + float(lse[a + i, j].abs()) * 2.0 ** -21
         return out, lse, tol, ltol
