@@ -1,10 +1,12 @@
 """The tree-verification operators on the GPU: the forms, sizes and calls that only a served batch or a long cache reaches."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_verify import check_attention, q, run_attention  # noqa: F401  (q is a fixture)
+import verify_helpers as vh
+from test_gpu_verify import check_attention, check_norm_rope, dn_inputs, dn_run, q, run_attention  # noqa: F401  (q is a fixture)
 from verify_helpers import DTYPES, Trees, gen, half_step, random_tree, tiny_step
 
 pytestmark = pytest.mark.gpu
@@ -48,6 +50,30 @@ def test_attention_pages_that_do_not_exist_in_a_long_run_of_small_ones(q):  # no
     with pytest.raises(q.StageError) as e:
         check_attention(q, t)
     assert e.value.code == -7
+
+
+def ragged(n, seed):
+    """n trees: empty ones, single tokens, small trees and a few of several M tiles, over caches from none to 3000 rows."""
+    g = gen(seed)
+    size = torch.tensor([0, 1, 1, 1, 3, 7, 40])[torch.randint(0, 7, (n,), generator=g)].tolist()
+    ctx = torch.randint(0, 60, (n,), generator=g).tolist()
+    size[n // 3], ctx[n // 3], ctx[n - 1] = 70, 3000, 900
+    size[n - 1] = 0                                      # a long cache that nobody asks for
+    return Trees(ctx, [random_tree(m, g) for m in size], 4, 1, 64, 32, torch.bfloat16, seed=seed, extra_rows=2)
+
+
+@pytest.mark.parametrize("n", [32, 33, 100, 255, 256, 257])
+def test_attention_batches_that_a_cta_plans_for_itself(q, n):  # noqa: F811
+    """Up to 32 trees are planned by a warp, up to 256 by every CTA, more by a kernel of their own."""
+    check_attention(q, ragged(n, n))
+
+
+@pytest.mark.parametrize("n", [40, 200])
+def test_attention_large_batches_of_equal_trees_of_several_tiles(q, n):  # noqa: F811
+    """Trees of two M tiles each, for which a group of CTAs has one for each."""
+    g = gen(n)
+    check_attention(q, Trees(torch.randint(0, 150, (n,), generator=g).tolist(), [random_tree(17, g) for _ in range(n)], 8, 1, 64, 16,
+                             torch.float16, seed=n))
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
@@ -116,6 +142,73 @@ def test_norm_rope_of_a_view_whose_width_is_not_a_multiple_of_16_bytes(q, src, n
         assert all(torch.equal(a, b) for a, b in zip(run(full[:, :width]), want))
 
 
+@pytest.mark.parametrize("src,dst", [("f32", "f16"), ("f32", "bf16"), ("f16", "f16"), ("f16", "bf16"), ("bf16", "bf16"), ("bf16", "f16")])
+@pytest.mark.parametrize("dim,rope", [(256, 64), (256, 256), (128, 128), (128, 48), (64, 64), (64, 32), (64, 0), (128, 0), (256, 200)])
+def test_norm_rope_of_many_rows(q, src, dst, dim, rope):  # noqa: F811
+    """Four passes per warp: 2501 rows of 9 vectors, the last pass and the last CTA partly filled."""
+    check_norm_rope(q, 2501, 7, 1, dim, rope, src, dst, seed=dim + rope)
+
+
+def test_norm_rope_of_many_strided_rows(q):  # noqa: F811
+    check_norm_rope(q, 2501, 6, 2, 128, 64, "bf16", "bf16", pad=24, offsets=(512, 0, 256))
+
+
+# ------------------------------------------------------------------ DeltaNet
+
+def served(n, seed, most=40):
+    """n trees of 0 to `most` tokens, some with padded ones, the largest not first."""
+    g = gen(seed)
+    size = torch.randint(0, 4, (n,), generator=g).tolist()
+    size[n - 2], size[1] = most, 17
+    trees = [random_tree(m, g) for m in size]
+    trees[1][5], trees[1][9] = -2, -2
+    assert max(len(vh.lineage(t, i) or []) for t in trees for i in range(len(t))) <= 13
+    return trees
+
+
+# 13 trees of 6 heads, or 2 of 48, are as many CTAs as take 32 rows each; beyond 32 trees they are not ordered by size
+@pytest.mark.parametrize("n,Hk,Hv", [(13, 2, 6), (32, 2, 4), (33, 1, 4), (40, 2, 2), (2, 16, 48), (3, 16, 48)])
+def test_deltanet_tree_batches_match_the_64_bit_form(q, n, Hk, Hv):  # noqa: F811
+    assert Hv * 4 * n > 2 * 148
+    parents = served(n, n) if n > 3 else [random_tree(18, gen(2)), [-1, -2, 0], [-1, 0, 0]][:n]
+    y, states, starts, parent = dn_inputs(parents, Hk, Hv, 5, n, extra=2)
+    index = [(3 * b) % 6 - 1 for b in range(n)]
+    o, snaps = dn_run(q, y, states, starts, parent, index, Hk, Hv)
+    ro, rs = vh.deltanet_tree(y, starts, parent.tolist(), states, index, Hk, Hv)
+    end = starts[-1]
+    dead = np.isnan(rs[:end]).any((1, 2, 3))
+    assert dead.any()
+    for r in range(end):                                 # the tolerance of test_deltanet_tree_matches_the_64_bit_form
+        if dead[r]:
+            assert bool((o[r] == 0).all()) and bool((snaps[r] == 9).all())
+        else:
+            assert np.abs(snaps[r].numpy() - rs[r]).max() <= 2.0 ** -16 * max(1, np.abs(rs[r]).max())
+            assert np.abs(o[r].numpy() - ro[r]).max() <= 2.0 ** -16 * max(1, np.abs(ro[r]).max())
+    assert bool((o[end:] == 9).all()) and bool((snaps[end:] == 9).all())
+    q.qhl_sync()
+
+
+@pytest.mark.parametrize("n,Hk,Hv,most", [(13, 2, 6, 40), (40, 2, 2, 128), (2, 16, 48, 35)])
+def test_deltanet_tree_paths_in_a_batch_have_the_bits_of_the_chained_step(q, n, Hk, Hv, most):  # noqa: F811
+    g = gen(most)
+    parents = [random_tree(int(m), g) for m in torch.randint(1, 4, (n,), generator=g)]
+    parents[n - 1] = random_tree(most, g)
+    y, states, starts, parent = dn_inputs(parents, Hk, Hv, 2, n)
+    o, snaps = dn_run(q, y, states, starts, parent, [b % 2 for b in range(n)], Hk, Hv)
+    for b in (0, n - 1):
+        tree = parents[b]
+        deepest = max(range(len(tree)), key=lambda i: len(vh.lineage(tree, i)))
+        for leaf in {len(tree) - 1, deepest}:
+            S = states[b % 2:b % 2 + 1].cuda().contiguous()
+            for i in vh.lineage(tree, leaf)[::-1]:
+                r = starts[b] + i
+                s1, o1 = torch.empty(1, Hv, 128, 128, device="cuda"), torch.empty(1, Hv * 128, device="cuda")
+                q.qhl_deltanet_step(Hk, Hv, y[r:r + 1].cuda(), S, s1, o1)
+                assert torch.equal(o1[0].cpu(), o[r]) and torch.equal(s1[0].cpu(), snaps[r])
+                S = s1
+    q.qhl_sync()
+
+
 # --------------------------------------------------------------------- pages
 
 def test_strides_along_an_axis_of_one_element_do_not_count(q):  # noqa: F811
@@ -153,4 +246,33 @@ def test_pages_needs_beyond_32_bits_are_refused(q):  # noqa: F811
     q.qhl_pages_extend(kv, seqs, add, status)
     assert status.tolist() == [0] + [-3] * (S - 1)
     assert kv.held.tolist() == [7] + [0] * (S - 1) and kv.refs.tolist() == [1] * 7 + [0] and table[0, :7].tolist() == list(range(7))
+    q.qhl_sync()
+
+
+def test_pages_beyond_2_31_elements_are_copied_and_written(q):  # noqa: F811
+    """A pool of more than 2^31 elements whose last pages are used: a shared page is copied among them, a path committed."""
+    n_pages, H, P, D = 33000, 4, 64, 256
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    k = torch.empty(1, n_pages, H, P, D, dtype=torch.float16, device="cuda")
+    v = torch.empty_like(k)
+    assert k[0, n_pages - 4].data_ptr() - k.data_ptr() > 2 * 2 ** 31
+    old, new, after = n_pages - 2, n_pages - 4, n_pages - 3
+    refs = torch.ones(n_pages, dtype=torch.int32, device="cuda")
+    refs[old], refs[new], refs[after] = 2, 0, 0
+    for c, base in ((k, 1), (v, 2)):
+        c[0, old:old + 1] = torch.randn(1, H, P, D, generator=gen(base)).half().cuda()
+        c[0, new], c[0, after] = 7, 7
+    kv = q.KvPages(k, v, i32([[old, -1], [old, -1]]), i32([40, 40]), i32([1, 1]), refs)
+    status = i32([9])
+    q.qhl_pages_extend(kv, i32([1]), i32([30]), status)
+    assert status.tolist() == [0] and kv.table.tolist() == [[old, -1], [new, after]] and refs[old:].tolist() == [1, 1]
+    for c in (k, v):
+        assert torch.equal(c[0, new, :, :40], c[0, old, :, :40]) and bool((c[0, new, :, 40:] == 7).all()) and bool((c[0, after] == 7).all())
+    kn, vn = (torch.randn(1, 30, H, D, generator=gen(s)).half().cuda() for s in (3, 4))
+    path = torch.randperm(30, generator=gen(5)).tolist()
+    q.qhl_pages_commit(kv, i32([1]), i32([0, 30]), i32([path]), i32([30]), i32([40]), kn, vn, status)
+    assert status.tolist() == [0] and kv.lens.tolist() == [40, 70]
+    for c, x in ((k, kn), (v, vn)):
+        rows = torch.cat([c[0, new, :, 40:], c[0, after, :, :6]], 1)
+        assert torch.equal(rows, x[0, path].transpose(0, 1)) and bool((c[0, after, :, 6:] == 7).all())
     q.qhl_sync()
