@@ -276,3 +276,78 @@ def test_pages_beyond_2_31_elements_are_copied_and_written(q):  # noqa: F811
         rows = torch.cat([c[0, new, :, 40:], c[0, after, :, :6]], 1)
         assert torch.equal(rows, x[0, path].transpose(0, 1)) and bool((c[0, after, :, 6:] == 7).all())
     q.qhl_sync()
+
+
+# ------------------------------------------- a step of a layer, and its oracle
+
+def test_a_layer_of_the_stage_as_a_tree_over_pages(q):  # noqa: F811
+    """The in-projections of the 27B-class shapes (quantised GEMV), then the tree operators, against the oracle's mixers run
+    along every path: an attention layer over 100 cached rows in pages, and a DeltaNet layer."""
+    import oracle
+    import synth
+    from synth import FULL, Q4_0
+    Hq, H, D, ctx, P, seed = FULL.att_q_heads, FULL.att_kv_heads, FULL.att_dim, 100, 64, 7
+    tree = [-1, 0, 0, 2, 1, -1]
+    n = len(tree)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    x = oracle.rmsnorm(synth.hidden(FULL, seed, 0, n), np.ones(FULL.hidden), FULL.eps).astype(np.float32)
+    t = {**synth.layer_tensors(FULL, Q4_0, seed, 2), **synth.layer_tensors(FULL, Q4_0, seed, 3)}
+
+    def project(name, rows):
+        W = t[name]
+        packed = torch.empty(q.qhl_packed_bytes(Q4_0, rows, FULL.hidden), dtype=torch.uint8, device="cuda")
+        q.qhl_repack(Q4_0, rows, FULL.hidden, torch.from_numpy(np.ascontiguousarray(W).reshape(-1)).cuda(), packed)
+        y = torch.empty(n, rows, device="cuda")
+        q.qhl_qgemv(Q4_0, rows, FULL.hidden, packed, torch.from_numpy(x).cuda(), y)
+        return y, oracle.qgemv(Q4_0, W, x)
+
+    # attention: y is q | gate | k | v
+    y, ry = project("blk.3.attn_in", FULL.attn_in_rows)
+    gq, gk = t["blk.3.attn_q_norm"], t["blk.3.attn_k_norm"]
+    K, V = synth.kv_prefill(FULL, seed, 3, ctx, ctx + n)
+    k, v = (torch.from_numpy(np.pad(c[:, :ctx], ((0, 0), (0, 2 * P - ctx), (0, 0)), constant_values=np.nan).reshape(H, 2, P, D)).permute(1, 0, 2, 3)[None]
+            .contiguous().cuda() for c in (K, V))
+    kv = q.KvPages(k, v, i32([[0, 1]]), i32([ctx]), i32([2]), i32([1, 1]))
+    pos = [ctx + len(vh.lineage(tree, i)) - 1 for i in range(n)]
+    qq, out = (torch.empty(n, Hq, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    kn, vn = (torch.empty(n, H, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    q.qhl_qk_norm_rope(Hq, H, D, FULL.rope_dims, FULL.rope_theta, FULL.eps, y, i32(pos), torch.from_numpy(gq).cuda(), torch.from_numpy(gk).cuda(), qq, kn, vn)
+    q.qhl_tree_attention(kv, 0, i32([0]), i32([0, n]), i32(tree), n, qq, kn, vn, out)
+    gate = torch.sigmoid(y[:, Hq * D:2 * Hq * D].double()).cpu().numpy()
+    got = out.double().cpu().numpy().reshape(n, -1) * gate
+    u = half_step(torch.float16)
+    for i in range(n):
+        line = vh.lineage(tree, i)[::-1]
+        Kp, Vp = K.copy(), V.copy()
+        for j, node in enumerate(line):                  # the oracle keeps one chain: its path
+            ref = oracle.attention_token(ry[node], ctx + j, Kp, Vp, gq, gk, FULL)
+        end = ctx + len(line)
+        qi = oracle.rope(oracle.rmsnorm(ry[i][:Hq * D].reshape(Hq, D), gq, FULL.eps), pos[i], FULL.rope_dims, FULL.rope_theta)
+        for h in range(Hq):
+            Kh, Vh = Kp[h // (Hq // H), :end].astype(np.float64), Vp[h // (Hq // H), :end].astype(np.float64)
+            s = Kh @ qi[h] / 16
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            # q is rounded to f16 (u), a drafted k and v may be one rounding apart from the oracle's (2 u each), the projections
+            # and the f32 sums are good to 2^-14 of their magnitudes; the errors of different elements of q and k are
+            # independent, but the bound adds them up
+            ds = (3 * u + 2.0 ** -14) * (np.abs(Kh) @ np.abs(qi[h])).max() / 16
+            A = w @ np.abs(Vh)
+            tol = (A * (2 * ds + 3.01 * u + 2.0 ** -14) + u * np.abs(w @ Vh)) * gate[i, h * D:(h + 1) * D] + 2.0 ** -14 * A
+            assert (np.abs(got[i, h * D:(h + 1) * D] - ref[h * D:(h + 1) * D]) <= tol).all()
+            # and on the whole: independent errors of 256 elements of q and k leave a few half steps of the output's size
+            assert oracle.max_rel_err(got[i, h * D:(h + 1) * D], ref[h * D:(h + 1) * D]) <= 8 * u
+
+    # DeltaNet: y is q | k | v | b | a
+    y, ry = project("blk.2.dn_in", FULL.dn_in_rows)
+    S0 = synth.dn_state(FULL, seed, 2)
+    snaps, o = torch.empty(n, FULL.dn_v_heads, 128, 128, device="cuda"), torch.empty(n, FULL.dn_o, device="cuda")
+    q.qhl_deltanet_tree(FULL.dn_k_heads, FULL.dn_v_heads, y, i32([0, n]), i32(tree), n, torch.from_numpy(S0)[None].cuda(), i32([0]), snaps, o)
+    for i in range(n):
+        S = S0.astype(np.float64)
+        for node in vh.lineage(tree, i)[::-1]:
+            S, ro = oracle.deltanet_token(S, *oracle.split_dn_in(ry[node], FULL), FULL)
+        assert oracle.max_rel_err(o[i].cpu().numpy(), ro.reshape(-1)) <= 2e-3          # the stage's own bounds
+        for h in range(FULL.dn_v_heads):
+            assert oracle.max_rel_err(snaps[i, h].cpu().numpy(), S[h]) <= 2e-3
+    q.qhl_sync()
