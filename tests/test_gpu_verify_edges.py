@@ -123,6 +123,45 @@ def test_attention_f16_weights_of_a_long_tail_are_kept(q, dim):  # noqa: F811
     q.qhl_sync()
 
 
+@pytest.mark.parametrize("kv_heads,group,nodes,ctx", [
+    (149, 1, [2], [130]),                                # more heads than CTAs, and a prime number of them
+    (256, 1, [1, 3], [70, 0]),
+    (1, 128, [128], [40]),                               # 128 M tiles
+    (1, 128, [128, 1, 2], [40, 700, 9]),
+    (2, 100, [77], [200]),                               # a group that is no divisor of a tile's rows
+])
+def test_attention_the_most_heads_and_tiles(q, kv_heads, group, nodes, ctx):  # noqa: F811
+    g = gen(sum(nodes))
+    check_attention(q, Trees(ctx, [random_tree(n, g) for n in nodes], kv_heads * group, kv_heads, 64, 16, torch.float16, seed=kv_heads))
+
+
+def test_attention_the_most_trees(q):  # noqa: F811
+    g = gen(1)
+    size = torch.randint(0, 3, (2048,), generator=g).tolist()
+    check_attention(q, Trees(torch.randint(0, 40, (2048,), generator=g).tolist(), [random_tree(m, g) for m in size], 2, 1, 64, 16, torch.bfloat16, seed=6))
+
+
+def test_attention_calls_on_two_streams_at_once(q):  # noqa: F811
+    """Calls that overlap have scratch of their own, also where the caller gives none."""
+    t = [Trees([c, 60], [random_tree(9, gen(c)), [-1]], 6, 2, 256, 64, torch.float16, seed=c) for c in (5000, 3001)]
+    want = [run_attention(q, x) for x in t]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    calls = []
+    for x in t:
+        kv = q.KvPages(x.k.cuda(), x.v.cuda(), x.table.cuda(), x.lens.cuda(), x.held.cuda(), x.refs.cuda())
+        ins = [y.cuda() for y in (x.seqs, x.q_start, x.parent, x.q, x.k_new, x.v_new)]
+        calls.append((kv, ins, [torch.zeros(x.rows, 6, 256, dtype=x.dtype, device="cuda") for _ in range(20)], x))
+    torch.cuda.synchronize()
+    for r in range(20):
+        for (kv, ins, out, x), s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                q.qhl_tree_attention(kv, 0, *ins[:3], x.max_nodes, *ins[3:], out[r], scale=x.scale)
+    torch.cuda.synchronize()
+    for (_, _, out, _), w in zip(calls, want):
+        assert all(torch.equal(o.cpu(), w[0]) for o in out)
+    q.qhl_sync()
+
+
 # ------------------------------------------------------------- norm and rope
 
 @pytest.mark.parametrize("src", ["f32", "f16", "bf16"])
