@@ -352,8 +352,11 @@ int qhl_qgemv_noalloc(int qtype, int rows, int cols, const void* packed_dev, con
  * Drafts are checked together in one batched pass (SwarmLLM README, feature
  * list); these calls do that for a tree of alternatives instead of one chain,
  * for a batch of sequences whose caches share a pool of pages.  The pages of
- * text name no tree and no paged cache; the arithmetic is that of the stage
- * (QK-norm, partial RoPE, GQA attention, the gated delta rule).
+ * text name no tree and no paged cache; the operators are the stage's (QK-norm,
+ * partial RoPE, GQA attention, the gated delta rule).  The gated delta rule has
+ * the bits of qhl_deltanet_step.  Attention has fewer than the stage's own, which
+ * carries queries and softmax weights in two f16 parts each (about 22 bits): here
+ * both are held in the cache's 16-bit type.
  *
  * A batch of trees: the tokens of entry b are rows q_start[b] ..
  * q_start[b + 1] - 1 of every per-token tensor (q_start_dev: int32
@@ -371,6 +374,12 @@ int qhl_qgemv_noalloc(int qtype, int rows, int cols, const void* packed_dev, con
  * on the current device, allocates nothing on the device and may be captured
  * into a graph (make one call before the first capture: it looks up the error
  * word and sets kernel attributes).
+ *
+ * Results are functions of a call's inputs, not of timing.  Norm + rotation and
+ * the delta rule give a token the same bits whatever else the call holds.
+ * Attention does not: it splits its keys by the lengths of the whole batch, so a
+ * token's last bits may change with the other sequences and drafts of the call
+ * (unlike the stage, whose verify pass has the bits of its single-token passes).
  * ------------------------------------------------------------------------- */
 
 /* 16- and 32-bit element types. */
@@ -378,9 +387,10 @@ typedef enum { QHL_F32 = 0, QHL_F16 = 1, QHL_BF16 = 2 } qhl_dtype;
 
 /* A KV cache in pages.  Element (layer, page, head, row, d) of k_dev and of
  * v_dev is at layer * stride_layer + page * stride_page + head * stride_head +
- * row * stride_row + d (in elements): any order of the axes, a stage's
- * contiguous [kv_heads, max_ctx, dim] cache included (stride_page = page_rows *
- * dim).  Strides are multiples of 8 elements, the bases 16-byte aligned, and
+ * row * stride_row + d (in elements): any order of the axes, a contiguous
+ * [kv_heads, max_ctx, dim] cache included (stride_page = page_rows * dim; a
+ * stage's own cache has this form, but its memory stays the stage's:
+ * stage_get_kv copies it out).  Strides are multiples of 8 elements, the bases 16-byte aligned, and
  * rows of one page do not overlap.  dtype QHL_F16 or QHL_BF16; dim 64, 128 or
  * 256; page_rows 16, 32, 64, 128 or 256.
  * Sequence s (0 <= s < n_seqs) has len_dev[s] committed rows, row r in page
@@ -436,8 +446,8 @@ size_t qhl_tree_attention_workspace(const qhl_kv_pages* kv, int n_q_heads, int n
  * [n_rows][n_q_heads], the natural logarithm of the sum of exp(scale * q k^T),
  * -inf where nothing is seen.  A hidden draft's infinities and NaN do not reach
  * the tokens that do not see it, nor do those of cache rows beyond len.
- * n_batch 1..2048, max_nodes 1..128, n_q_heads / kv_heads at most 128, scale
- * positive.  Every base is 16-byte aligned and every stride a multiple of 8.
+ * n_batch 1..2048, max_nodes 1..128, n_q_heads / kv_heads at most 128, n_batch *
+ * n_q_heads * max_nodes at most 2^26, scale positive.  Every base is 16-byte aligned and every stride a multiple of 8.
  * Scores, softmax statistics and sums are f32; the softmax weights are rounded
  * to the cache's type for the product with v. */
 int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_rows, int n_batch, int max_nodes,

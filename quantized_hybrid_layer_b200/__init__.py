@@ -396,8 +396,9 @@ def qhl_deltanet_step(Hk: int, Hv: int, y, s_in, snaps, o, stream=None):
 
 
 def qhl_sync(stream=None):
-    """Wait for the stream; raise StageError(STAGE_E_DEVICE) if a qhl_qgemv /
-    qhl_qgemv_noalloc kernel's bounded wait ran out since the last qhl_sync."""
+    """Wait for the stream; raise StageError(STAGE_E_DEVICE) if, since the last qhl_sync on
+    the current device, a bounded wait of a qhl_* kernel ran out there, or an index that
+    lives on the device (a page, a parent, a row offset) was out of range."""
     _check_qhl(lib().qhl_sync(_stream(stream)))
 
 

@@ -25,8 +25,8 @@
 //
 // The inputs of 16 tokens at a time come by asynchronous copies, a block ahead (as
 // loads in turn they took 3.3 us a block).  Measured: one tree of 16 tokens and 48
-// heads 15.4 us for 53.5 MB (3.5 TB/s: the chain of tokens), eight ragged trees,
-// 426 MB, 79.7 us (5.3 TB/s; a plain fill of 400 MB reaches 7.2 TB/s).
+// heads 14.5 us for 54.5 MB (3.8 TB/s: the chain of tokens), eight ragged trees,
+// 427 MB, 81 to 86 us (5.0 to 5.3 TB/s; a plain fill of 400 MB reaches 7.2 TB/s).
 //
 // No early start of the kernel behind this one (20.0 us against 24.3): its waiting
 // CTAs, spread unevenly, would take this kernel's places.
@@ -318,9 +318,9 @@ extern "C" int qhl_deltanet_tree(int Hk, int Hv, const float* y_dev, int n_rows,
   cudaError_t e = verify_error_word(&a.err);
   if (e != cudaSuccess) return verify_cuda_err(me, e);
   // Few CTAs: 16 rows each, spread more evenly, with all the registers that the
-  // kernel wants (one tree of 16 tokens, 48 heads: 15.4 us, with 32 rows 16.5 us).
-  // Many: 32 rows and registers for three CTAs per SM (eight such trees: 78.6 us,
-  // with two per SM 84.2 us).
+  // kernel wants (one tree of 16 tokens, 48 heads: 14.2 us, with 32 rows 16.9 us).
+  // Many: 32 rows and registers for three CTAs per SM (eight such trees: 79.4 us,
+  // with two per SM 81.7 us, with 16 rows 84.4 us).
   const bool few = (long long)Hv * 4 * n_batch <= 2 * 148;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   e = few ? launch_ex(dn_tree_kernel<kDtRows, 16, 4>, dim3(Hv * 8, n_batch), dim3(128), 0, s, true, a)

@@ -15,10 +15,10 @@
 // instructions per warp), and theta^(-2 i / R) is a product of at most seven factors
 // theta^(-2^(j+1) / R), one for each bit j of i, so no table is read.
 //
-// Measured: 8191 tokens of 24 + 4 + 4 heads of 256, f32 to bf16, 71.1 us, 5.7 TB/s
-// (0.87 of the measured copy); of 96 + 8 + 8 heads of 64 59.4 us, 5.9 TB/s; from
-// bf16 rows 4.0 to 4.6 TB/s, bound by the instructions.  One token: 2.4 us of GPU
-// time, a launch.
+// Measured: 8191 tokens of 24 + 4 + 4 heads of 256, f32 to bf16, 72 to 76 us, 5.3 to
+// 5.6 TB/s (0.81 to 0.86 of the measured copy); of 96 + 8 + 8 heads of 64 61 us, 5.8
+// TB/s; from 16-bit rows 4.1 to 4.6 TB/s, bound by the instructions.  One token: 3.1
+// to 3.7 us a call, a launch.
 #include <algorithm>
 
 #include "launch.h"
@@ -187,9 +187,9 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeArgs a) {
 template <typename SRC, typename DST, int D>
 static cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
   // Few vectors, all in one wave of warps: one pass per warp (one row of 32 heads
-  // 3.2 us a call, 64 rows 3.2 us; with four passes 4.0 and 5.1 us).  Many: four, so
+  // 3.3 us a call, 64 rows 3.3 us; with four passes 4.1 and 4.4 us).  Many: four, so
   // that a warp has four loads per lane in flight and forms the angles once (512 rows
-  // 6.0 us, 8191 rows 71.1 us; with one pass 6.9 and 88.0 us).
+  // 6.0 us, 8191 rows 72.1 us; with one pass 6.7 and 88.0 us).
   constexpr int NP = 256 / D;
   const int nvec = a.hq + 2 * a.hkv, one = (nvec + NP - 1) / NP, four = (nvec + 4 * NP - 1) / (4 * NP);
   const bool few = (long long)a.n_rows * one <= 148 * 48;

@@ -14,8 +14,8 @@
 // committed rows; bound by those rows, read and written once.  commit: one CTA
 // per (tree, layer, K or V), 16-byte moves, bound by the accepted rows.
 // Measured: 96 branches of 12 sequences freed, forked and extended, 16 layers of
-// 4 heads x 256: 67.1 us, 6.7 TB/s of copied rows; 2 branches of one 12.4 us, four
-// launches; 8 accepted paths of up to 16 tokens 5.6 us.
+// 4 heads x 256: 67.3 us, 6.7 TB/s of copied rows; 2 branches of one 12.5 us, four
+// launches; 8 accepted paths of up to 16 tokens 5.7 us.
 // Every kernel is launched as a programmatic dependent of the one before it on
 // the stream and waits for that one's end before it reads anything, which hides
 // most of a launch (about 1 us of a chain of short calls).

@@ -21,12 +21,14 @@
 // 16 tokens over 65536 rows), and so does p, over the S it came from, as the A
 // operand of the second product.
 //
-// Measured (B200; 6543 GB/s and 1624 TFLOP/s are the measured peaks): 16 tokens of
-// 24 heads over 262001 rows 188 us, 5.7 TB/s; 24 trees of 12 tokens over 16384 rows
-// at 128 dimensions 254 us, 6.4 TB/s; 64 tokens over 4 x 65536 rows 385 us, 1.07
-// PFLOP/s, where the power cap holds the clock at 1.5 to 1.65 GHz and a tile of 64
-// keys takes about 1700 cycles (S: 16 MMAs of N = 64 that cost as much as N = 128
-// would; a second S of 128 columns does not fit beside O and Q).
+// Measured (B200, passes one after another; 6543 GB/s and 1624 TFLOP/s are the
+// measured peaks): 16 tokens of 24 heads over 262001 rows 193 us, 5.6 TB/s; 32 single
+// tokens over 16384 rows each 336 us, 6.4 TB/s; 24 trees of 12 tokens over 16384 rows
+// at 128 dimensions 288 us, 5.6 TB/s (253 us after a pause); 64 tokens over 4 x 65536
+// rows 460 us, 0.90 PFLOP/s (395 us after a pause), where the power cap holds the
+// clock at 1.5 to 1.65 GHz and a tile of 64 keys takes about 1700 cycles (S: 16 MMAs
+// of N = 64 that cost as much as N = 128 would; a second S of 128 columns does not fit
+// beside O and Q).
 //
 // Work split: the CTAs take equal runs of key tiles (see "planning"), from lengths
 // that they read on the device, so one captured graph serves every length.  What is
