@@ -192,6 +192,22 @@ def test_norm_rope_of_many_strided_rows(q):  # noqa: F811
     check_norm_rope(q, 2501, 6, 2, 128, 64, "bf16", "bf16", pad=24, offsets=(512, 0, 256))
 
 
+@pytest.mark.parametrize("src,dim,rope", [("f32", 256, 64), ("bf16", 128, 128), ("f16", 64, 32)])
+def test_norm_rope_gives_a_row_the_same_bits_alone_and_among_many(q, src, dim, rope):  # noqa: F811
+    st, n = {"f32": torch.float32, **DTYPES}[src], 2501
+    y = torch.randn(n, 16 * dim, generator=gen(dim)).to(st).cuda()
+    pos = torch.randint(0, 262144, (n,), generator=gen(2), dtype=torch.int32).cuda()
+    gamma = torch.randn(2, dim, generator=gen(3)).cuda()
+
+    def run(rows):
+        out = [torch.zeros(rows.stop - rows.start, h, dim, dtype=torch.bfloat16, device="cuda") for h in (7, 1, 1)]
+        return q.qhl_qk_norm_rope(7, 1, dim, rope, 1e7, 1e-6, y[rows], pos[rows], gamma[0], gamma[1], *out)
+
+    many = run(slice(0, n))
+    for r in (0, 1, 1250, n - 1):
+        assert all(torch.equal(a[0], b[r]) for a, b in zip(run(slice(r, r + 1)), many))
+
+
 # ------------------------------------------------------------------ DeltaNet
 
 def served(n, seed, most=40):
