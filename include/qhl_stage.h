@@ -464,8 +464,9 @@ int qhl_tree_attention(const qhl_kv_pages* kv, int layer, int n_q_heads, int n_r
  * as in qhl_deltanet_step, with n_rows rows.  A padded token's o row is 0 and
  * its snapshot is not written.  Along a path the results are bit-identical to
  * qhl_deltanet_step.  The snapshots must not overlap the states that are read.
- * n_batch 1..2048, max_nodes 1..128; y_dev, states_dev, snaps_dev and o_dev
- * 16-byte aligned, 2 * Hv + the q, k, v widths a multiple of 4. */
+ * n_states at least 1, n_batch 1..2048, max_nodes 1..128; y_dev, states_dev,
+ * snaps_dev and o_dev 16-byte aligned, 2 * Hv + the q, k, v widths a multiple of
+ * 4. */
 int qhl_deltanet_tree(int Hk, int Hv, const float* y_dev, int n_rows, int n_batch, int max_nodes,
                       const int* q_start_dev, const int* parent_dev, const float* states_dev, int n_states,
                       const int* state_index_dev, float* snaps_dev, float* o_dev, void* stream);
